@@ -389,6 +389,118 @@ SSD_API ssd_status ssd_test_stall_prefill(uint64_t wait_ns);
  */
 SSD_API ssd_status ssd_set_timing_events(void* before_main, void* after_main);
 
+/*
+ * Decayed linear attention: a layer of H heads whose state is a Dk x Dv matrix
+ * with one constant decay per head -- the recurrence that state-space duality
+ * turns into masked attention, on plain queries, keys and values (no short
+ * conv, no dt, no gate).  Per token t and head h (key and value head
+ * h * kv_heads / H):
+ *     S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T
+ *     o_t = scale * q_t S_t
+ * The decay is a constant of the layer (log_decay <= 0, -inf keeps nothing of
+ * the past); it has no gradient here.  A non-finite value in a row reaches the
+ * other rows of its own sequence and head only: its later ones, and earlier
+ * ones of up to 127 rows before.
+ *
+ *   key_dim, value_dim  Dk, Dv: multiples of 8 from 8 to 128
+ *   dtype               SSD_BF16 or SSD_F32 (q, k, v, o and their gradients);
+ *                       states and log_decay are fp32
+ *   rows                batch * seqlen, or seqlen alone when packed; < 2^31 - 256
+ * Packed batches: cu_seqlens is a device array of batch + 1 non-decreasing row
+ * offsets, sequence s = rows cu_seqlens[s] .. cu_seqlens[s+1]-1; rows outside
+ * every sequence are neither used nor written.  Offsets out of order or out of
+ * range are reported by ssd_device_status (SSD_ERR_SHAPE) and that sequence is
+ * taken as empty.
+ */
+typedef struct {
+    int64_t batch;     /* sequences                                             */
+    int64_t seqlen;    /* tokens per sequence; all rows when packed             */
+    int32_t nheads;    /* H                                                     */
+    int32_t kv_heads;  /* heads of k and v; nheads % kv_heads == 0              */
+    int32_t key_dim;   /* Dk                                                    */
+    int32_t value_dim; /* Dv                                                    */
+} ssd_linear_attn_dims;
+
+/* Elements between consecutive tokens of q, k and v (a batch is seqlen rows): at least a row's
+ * width, multiples of 16 bytes.  Lets them be views of one projection's output. */
+typedef struct {
+    int64_t q, k, v;
+} ssd_linear_attn_strides;
+
+/*
+ * Chunked form over whole prompts.
+ *   q           [batch][seqlen][H][Dk], k [..][kv_heads][Dk], v [..][kv_heads][Dv]  (or [rows][..])
+ *   strides     row strides of q, k, v, or NULL for contiguous rows
+ *   cu_seqlens  device offsets of a packed batch, or NULL
+ *   init_state  [batch][H][Dk][Dv] fp32 or NULL for zeros; may equal final_state
+ *   o           [batch][seqlen][H][Dv] dtype (out), 32-byte aligned
+ *   final_state [batch][H][Dk][Dv] fp32 (out): the state after each sequence's last token
+ *   workspace   ssd_linear_attn_prefill_workspace_bytes() bytes (may be NULL when that is 0);
+ *               two calls that may run at once need one each
+ */
+SSD_API size_t ssd_linear_attn_prefill_workspace_bytes(const ssd_linear_attn_dims* dims, ssd_dtype dtype, int packed);
+SSD_API ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* dims, ssd_dtype dtype, const float* log_decay,
+                                           float scale, const ssd_linear_attn_strides* strides,
+                                           const int64_t* cu_seqlens, const void* q, const void* k, const void* v,
+                                           const float* init_state, void* o, float* final_state, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of the chunked form: of sum(d_o * o) + sum(d_final_state * final_state).
+ * q, k, v, d_o contiguous; dq, dk, dv (out) laid out as q, k, v in dtype, 32-byte aligned (shared key
+ * and value heads: the sum over their query heads, taken in fp32).  init_state and d_final_state may be
+ * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.
+ */
+SSD_API size_t ssd_linear_attn_backward_workspace_bytes(const ssd_linear_attn_dims* dims, ssd_dtype dtype, int packed);
+SSD_API ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* dims, ssd_dtype dtype, const float* log_decay,
+                                            float scale, const int64_t* cu_seqlens, const void* q, const void* k,
+                                            const void* v, const float* init_state, const void* d_o,
+                                            const float* d_final_state, void* dq, void* dk, void* dv,
+                                            float* d_init_state, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * One token for each of `batch` sequences (dims->seqlen is ignored):
+ *   q [batch][H][Dk], k [batch][kv_heads][Dk], v [batch][kv_heads][Dv], state [batch][H][Dk][Dv] fp32
+ *   updated in place, o [batch][H][Dv] (out).
+ */
+SSD_API ssd_status ssd_linear_attn_decode_step(const ssd_linear_attn_dims* dims, ssd_dtype dtype,
+                                               const float* log_decay, float scale, const void* q, const void* k,
+                                               const void* v, float* state, void* o, void* stream);
+
+/*
+ * RMSNorm of every query and key head with the position rotation in the same pass.  Per token and head row x:
+ *     n = x * rsqrt(mean(x^2) + eps) * weight[channel]
+ *     (y_a, y_b) = (n_a cos - n_b sin, n_b cos + n_a sin) for pair p of the first rot_dim channels, y = n elsewhere
+ * with the angle positions[token] * inv_freq[p], taken in fp64.  Pair p is channels (p, p + rot_dim/2), or
+ * (2p, 2p + 1) when interleaved.
+ *   q [tokens][q_heads][head_dim], k [tokens][k_heads][head_dim]: dtype SSD_BF16 or SSD_F32; strides as above
+ *   (elements between tokens) or NULL; q_weight, k_weight [head_dim] fp32; positions [tokens] int64;
+ *   inv_freq [rot_dim / 2] fp32; q_out, k_out contiguous (a contiguous input may be its own output).
+ *   head_dim: a multiple of 8 up to 256; rot_dim: a multiple of 8 up to head_dim (0: no rotation).
+ * The backward takes the gradients of q_out and k_out (contiguous) and the forward's inputs, and writes dq, dk
+ * (contiguous, dtype) and the fp32 weight gradients; deterministic.
+ */
+typedef struct {
+    int64_t tokens;
+    int32_t q_heads, k_heads, head_dim, rot_dim;
+    int32_t interleaved;
+} ssd_qk_dims;
+typedef struct {
+    int64_t q, k;
+} ssd_qk_strides;
+SSD_API ssd_status ssd_qk_norm_rope(const ssd_qk_dims* dims, ssd_dtype dtype, float eps, const ssd_qk_strides* strides,
+                                    const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                    const int64_t* positions, const float* inv_freq, void* q_out, void* k_out,
+                                    void* stream);
+SSD_API size_t ssd_qk_norm_rope_backward_workspace_bytes(const ssd_qk_dims* dims);
+SSD_API ssd_status ssd_qk_norm_rope_backward(const ssd_qk_dims* dims, ssd_dtype dtype, float eps,
+                                             const ssd_qk_strides* strides, const void* dq_out, const void* dk_out,
+                                             const void* q, const void* k, const float* q_weight,
+                                             const float* k_weight, const int64_t* positions, const float* inv_freq,
+                                             void* dq, void* dk, float* dq_weight, float* dk_weight, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

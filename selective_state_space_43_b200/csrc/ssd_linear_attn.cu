@@ -1,0 +1,422 @@
+// ssd_linear_attn.cu -- decayed linear attention: the single-token step, the joining of segment states, the
+// sum of shared heads' gradients, and the C entry points (ssd_linear_attn_*).
+#include <math.h>
+
+#include "ssd.h"
+#include "ssd_common.cuh"
+#include "ssd_internal.h"
+#include "ssd_linear_attn.h"
+
+namespace ssd {
+namespace la {
+namespace {
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xFFFF0000u), __uint_as_float(a.y << 16),
+                       __uint_as_float(a.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// ---- one token ----------------------------------------------------------------------------------------------
+// S <- e^l S + k v^T, o = scale q S: every state element is read once and written once, two FMAs each, so the
+// step is bound by HBM.  One block per (sequence, head); a thread holds four value channels and walks the key
+// rows with eight 16-byte loads in flight; the rows' partial outputs are joined in shared memory in a fixed order.
+constexpr int kDecThreads = 256, kDecRows = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kDecThreads) decode_kernel(DecodeArgs a) {
+    __shared__ float4 red[kDecThreads];
+    __shared__ float sq[128], sk[128];
+    const int64_t b = blockIdx.x / a.H;
+    const int h = (int)(blockIdx.x - b * a.H), hk = h / (a.H / a.Hk), tid = threadIdx.x;
+    const int nq = a.Dv / 4, per = kDecThreads / nq;  // threads across a row, rows of a pass
+    const int r = tid / nq, c = (tid - r * nq) * 4;
+    const bool live = r < per;
+    float* S = a.state + (size_t)blockIdx.x * a.Dk * a.Dv;
+    if (tid < a.Dk) {
+        sq[tid] = to_f32(static_cast<const T*>(a.q)[(size_t)blockIdx.x * a.Dk + tid]) * a.scale;
+        sk[tid] = to_f32(static_cast<const T*>(a.k)[((size_t)b * a.Hk + hk) * a.Dk + tid]);
+    }
+    const float4 v = load4(static_cast<const T*>(a.v) + ((size_t)b * a.Hk + hk) * a.Dv + (live ? c : 0));
+    const float decay = decay_pow(a.log_decay[h], 1);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    for (int r0 = live ? r : a.Dk; r0 < a.Dk; r0 += per * kDecRows) {
+        float4 x[kDecRows];
+#pragma unroll
+        for (int i = 0; i < kDecRows; ++i)
+            if (r0 + i * per < a.Dk) x[i] = load4(S + (size_t)(r0 + i * per) * a.Dv + c);
+#pragma unroll
+        for (int i = 0; i < kDecRows; ++i) {
+            const int d = r0 + i * per;
+            if (d < a.Dk) {
+                const float kd = sk[d], qd = sq[d];
+                x[i].x = fmaf(decay, x[i].x, kd * v.x);
+                x[i].y = fmaf(decay, x[i].y, kd * v.y);
+                x[i].z = fmaf(decay, x[i].z, kd * v.z);
+                x[i].w = fmaf(decay, x[i].w, kd * v.w);
+                store4(S + (size_t)d * a.Dv + c, x[i]);
+                o.x = fmaf(qd, x[i].x, o.x);
+                o.y = fmaf(qd, x[i].y, o.y);
+                o.z = fmaf(qd, x[i].z, o.z);
+                o.w = fmaf(qd, x[i].w, o.w);
+            }
+        }
+    }
+    red[tid] = o;
+    __syncthreads();
+    if (tid < nq) {
+        float4 t = red[tid];
+        for (int i = 1; i < per; ++i) {
+            const float4 u = red[i * nq + tid];
+            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+        }
+        store4(static_cast<T*>(a.o) + (size_t)blockIdx.x * a.Dv + c, t);
+    }
+}
+
+// ---- joining segments ---------------------------------------------------------------------------------------
+// R <- e^{l n_i} R + (state of segment i alone), in scan order; four state elements per thread.
+__global__ void __launch_bounds__(256) combine_kernel(ScanArgs a) {
+    const int64_t b = blockIdx.x;
+    const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4, size = a.Dk * a.Dv;
+    const Span s = sequence_span(a, b);
+    if (!s.ok && h == 0 && e == 0) atomicOr(a.err, kErrBadSeqlens);
+    if (e >= size) return;
+    const float l = a.log_decay[h];
+    float4 R = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (a.init) {
+        const float* src = a.init + ((size_t)b * a.H + h) * size;
+        if (a.init_t) {
+            const float* t = src + (size_t)(e % a.Dv) * a.Dk + e / a.Dv;
+            R = make_float4(t[0], t[a.Dk], t[2 * a.Dk], t[3 * a.Dk]);
+        } else {
+            R = load4(src + e);
+        }
+    }
+    const int64_t nseg = (s.len + a.seg_len - 1) / a.seg_len, slot0 = first_slot(a, b, s);
+    const float whole = decay_pow(l, a.seg_len);
+    const float last = decay_pow(l, s.len - (nseg - 1) * a.seg_len);
+#pragma unroll 4
+    for (int64_t j = 0; j < nseg; ++j) {
+        const int64_t i = a.reverse ? nseg - 1 - j : j;
+        float* p = a.seg_state + ((size_t)(slot0 + i) * a.H + h) * size + e;
+        const float4 x = load4(p);
+        const float d = i == nseg - 1 ? last : whole;
+        store4(p, R);
+        R.x = fmaf(d, R.x, x.x);
+        R.y = fmaf(d, R.y, x.y);
+        R.z = fmaf(d, R.z, x.z);
+        R.w = fmaf(d, R.w, x.w);
+    }
+    if (a.final_state) store4(a.final_state + ((size_t)b * a.H + h) * size + e, R);
+}
+
+// ---- gradients of shared heads ------------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) group_sum_kernel(const float* src, T* dst, int64_t quads, int group, int width) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= quads) return;
+    const int per = width / 4;
+    const int64_t head = i / per;  // (row, head) of dst
+    const float* p = src + (head * group * per + (i - head * per)) * 4;
+    float4 t = load4(p);
+    for (int g = 1; g < group; ++g) {
+        const float4 u = load4(p + (size_t)g * width);
+        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+    store4(dst + i * 4, t);
+}
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {
+    const unsigned blocks = (unsigned)(a.batch * a.H);
+    if (a.bf16)
+        decode_kernel<__nv_bfloat16><<<blocks, kDecThreads, 0, st>>>(a);
+    else
+        decode_kernel<float><<<blocks, kDecThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_combine(const ScanArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)a.batch, a.H, (a.Dk * a.Dv + 1023) / 1024);
+    combine_kernel<<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_group_sum(const float* src, void* dst, int64_t rows, int heads, int group, int width, bool bf16,
+                             cudaStream_t st) {
+    const int64_t quads = rows * heads * (width / 4);
+    if (quads == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)((quads + 255) / 256);
+    if (bf16)
+        group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(src, static_cast<__nv_bfloat16*>(dst), quads, group,
+                                                                 width);
+    else
+        group_sum_kernel<float><<<blocks, 256, 0, st>>>(src, static_cast<float*>(dst), quads, group, width);
+    return cudaGetLastError();
+}
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Read one value at a time, so their own alignment is enough.
+bool offsets_aligned(const float* log_decay, const int64_t* cu_seqlens) {
+    return !(reinterpret_cast<uintptr_t>(log_decay) & 3u) && !(reinterpret_cast<uintptr_t>(cu_seqlens) & 7u);
+}
+
+ssd_status check_dims(const ssd_linear_attn_dims* d, ssd_dtype dtype) {
+    if (!d) return SSD_ERR_NULL;
+    if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_DTYPE;
+    if (d->batch < 0 || d->seqlen < 0) return SSD_ERR_SHAPE;
+    if (d->nheads <= 0 || d->kv_heads <= 0 || d->nheads % d->kv_heads != 0 || d->nheads > 65535) return SSD_ERR_SHAPE;
+    for (int w : {d->key_dim, d->value_dim})
+        if (w < 8 || w > 128 || w % 8 != 0) return SSD_ERR_SHAPE;
+    if (d->batch > (1LL << 31) - 1 || d->batch * (int64_t)d->nheads > (1LL << 31) - 1) return SSD_ERR_SHAPE;
+    return SSD_OK;
+}
+
+// Rows of all sequences; tensor-map row coordinates and the launches' slot counts are 32-bit.
+ssd_status count_rows(const ssd_linear_attn_dims* d, bool packed, int64_t* rows) {
+    constexpr int64_t most = (1LL << 31) - 256;
+    if (d->seqlen > most || (!packed && d->seqlen > 0 && d->batch > most / d->seqlen)) return SSD_ERR_SHAPE;
+    *rows = packed ? d->seqlen : d->batch * d->seqlen;
+    return SSD_OK;
+}
+
+struct Buffer {
+    const void* p;
+    uint64_t n;  // bytes
+};
+// A role's rows as the caller's buffer: `rows` rows `stride` elements apart, the last one `width` long.
+Buffer row_buffer(const void* p, int64_t rows, int64_t stride, int64_t width, uint64_t esize) {
+    return Buffer{p, rows > 0 ? ((uint64_t)(rows - 1) * stride + width) * esize : 0};
+}
+bool overlap(const Buffer& a, const Buffer& b) {
+    if (!a.p || !b.p || !a.n || !b.n) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.n && y < x + a.n;
+}
+template <int NO, int NI> bool outputs_alias(const Buffer (&outs)[NO], const Buffer (&ins)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = i + 1; j < NO; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+        for (int j = 0; j < NI; ++j)
+            if (overlap(outs[i], ins[j])) return true;
+    }
+    return false;
+}
+
+// One scan: whole sequences.
+cudaError_t launch_scan(ScanArgs a, cudaStream_t st) { return launch_scan_simt(a, kWhole, st); }
+
+}  // namespace
+}  // namespace la
+}  // namespace ssd
+
+using namespace ssd;
+using namespace ssd::la;
+
+extern "C" {
+
+size_t ssd_linear_attn_prefill_workspace_bytes(const ssd_linear_attn_dims* d, ssd_dtype dtype, int packed) {
+    (void)packed;
+    if (la::check_dims(d, dtype) != SSD_OK) return 0;
+    return 0;
+}
+
+ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* d, ssd_dtype dtype, const float* log_decay, float scale,
+                                   const ssd_linear_attn_strides* strides, const int64_t* cu_seqlens, const void* q,
+                                   const void* k, const void* v, const float* init_state, void* o, float* final_state,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    ssd_status st = la::check_dims(d, dtype);
+    if (st != SSD_OK) return st;
+    const bool packed = cu_seqlens != nullptr;
+    int64_t rows;
+    if ((st = count_rows(d, packed, &rows)) != SSD_OK) return st;
+    if (!isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!log_decay || (d->batch > 0 && !final_state)) return SSD_ERR_NULL;
+    if (d->batch > 0 && rows > 0 && (!q || !k || !v || !o)) return SSD_ERR_NULL;
+    for (const void* p : {q, k, v, (const void*)init_state, (const void*)final_state, (const void*)workspace})
+        if (!aligned16(p)) return SSD_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(o) & 31u) || !offsets_aligned(log_decay, cu_seqlens)) return SSD_ERR_ALIGN;
+    const int64_t H = d->nheads, Hk = d->kv_heads, Dk = d->key_dim, Dv = d->value_dim;
+    const uint64_t es = dtype == SSD_F32 ? 4 : 2;
+    ssd_linear_attn_strides rs{H * Dk, Hk * Dk, Hk * Dv};
+    if (strides) {
+        if (strides->q < rs.q || strides->k < rs.k || strides->v < rs.v) return SSD_ERR_SHAPE;
+        if (strides->q > (1LL << 32) || strides->k > (1LL << 32) || strides->v > (1LL << 32)) return SSD_ERR_SHAPE;
+        if (((strides->q | strides->k | strides->v) * (int64_t)es) & 15) return SSD_ERR_ALIGN;
+        rs = *strides;
+    }
+    const uint64_t state = (uint64_t)d->batch * H * Dk * Dv * 4;
+    const size_t need = ssd_linear_attn_prefill_workspace_bytes(d, dtype, packed);
+    {
+        const Buffer ins[] = {row_buffer(q, rows, rs.q, H * Dk, es), row_buffer(k, rows, rs.k, Hk * Dk, es),
+                              row_buffer(v, rows, rs.v, Hk * Dv, es), {log_decay, (uint64_t)H * 4},
+                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}, {workspace, need}};
+        const Buffer outs[] = {{o, (uint64_t)rows * H * Dv * es}, {final_state, state}};
+        if (outputs_alias(outs, ins)) return SSD_ERR_UNSUPPORTED;
+        if (init_state && init_state != final_state && overlap({init_state, state}, outs[1])) return SSD_ERR_UNSUPPORTED;
+        if (overlap({init_state, state}, outs[0])) return SSD_ERR_UNSUPPORTED;
+    }
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+    if (d->batch == 0) return SSD_OK;
+    ScanArgs a{};
+    a.q = q; a.k = k; a.v = v;
+    a.rs_q = rs.q; a.rs_k = rs.k; a.rs_v = rs.v;
+    a.gq = 1; a.gk = a.gv = (int)(H / Hk);
+    a.H = (int)H; a.Dk = (int)Dk; a.Dv = (int)Dv;
+    a.log_decay = log_decay;
+    a.qk_scale = a.inter_scale = scale;
+    a.w_scale = 1.f;
+    a.bf16 = dtype == SSD_BF16;
+    a.init = init_state;
+    a.final_state = final_state;
+    a.o = o;
+    a.batch = d->batch; a.L = d->seqlen; a.rows = rows;
+    a.cu = cu_seqlens;
+    if (!(a.err = device_error_flag())) return SSD_ERR_CUDA;
+    return launch_scan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+// Bytes of the fp32 per-head gradients of shared keys and values (none when every head has its own).
+static size_t group_bytes(const ssd_linear_attn_dims* d, int64_t rows) {
+    if (d->nheads == d->kv_heads) return 0;
+    return (size_t)rows * d->nheads * (d->key_dim > d->value_dim ? d->key_dim : d->value_dim) * 4;
+}
+
+size_t ssd_linear_attn_backward_workspace_bytes(const ssd_linear_attn_dims* d, ssd_dtype dtype, int packed) {
+    int64_t rows;
+    if (la::check_dims(d, dtype) != SSD_OK || count_rows(d, packed != 0, &rows) != SSD_OK) return 0;
+    return group_bytes(d, rows);
+}
+
+ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dtype, const float* log_decay, float scale,
+                                    const int64_t* cu_seqlens, const void* q, const void* k, const void* v,
+                                    const float* init_state, const void* d_o, const float* d_final_state, void* dq,
+                                    void* dk, void* dv, float* d_init_state, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+    ssd_status st = la::check_dims(d, dtype);
+    if (st != SSD_OK) return st;
+    const bool packed = cu_seqlens != nullptr;
+    int64_t rows;
+    if ((st = count_rows(d, packed, &rows)) != SSD_OK) return st;
+    if (!isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!log_decay) return SSD_ERR_NULL;
+    if (d->batch > 0 && rows > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return SSD_ERR_NULL;
+    for (const void* p : {q, k, v, d_o, (const void*)init_state, (const void*)d_final_state, (const void*)d_init_state,
+                          (const void*)workspace})
+        if (!aligned16(p)) return SSD_ERR_ALIGN;
+    for (const void* p : {dq, dk, dv})
+        if (reinterpret_cast<uintptr_t>(p) & 31u) return SSD_ERR_ALIGN;
+    if (!offsets_aligned(log_decay, cu_seqlens)) return SSD_ERR_ALIGN;
+    const int64_t H = d->nheads, Hk = d->kv_heads, Dk = d->key_dim, Dv = d->value_dim;
+    const uint64_t es = dtype == SSD_F32 ? 4 : 2, n = (uint64_t)rows;
+    const uint64_t state = (uint64_t)d->batch * H * Dk * Dv * 4;
+    const size_t need = ssd_linear_attn_backward_workspace_bytes(d, dtype, packed);
+    {
+        const Buffer ins[] = {{q, n * H * Dk * es}, {k, n * Hk * Dk * es}, {v, n * Hk * Dv * es}, {d_o, n * H * Dv * es},
+                              {init_state, state}, {d_final_state, state}, {log_decay, (uint64_t)H * 4},
+                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}, {workspace, need}};
+        const Buffer outs[] = {{dq, n * H * Dk * es}, {dk, n * Hk * Dk * es}, {dv, n * Hk * Dv * es},
+                               {d_init_state, state}};
+        if (outputs_alias(outs, ins)) return SSD_ERR_UNSUPPORTED;
+    }
+    if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+    if (d->batch == 0) return SSD_OK;
+
+    const int group = (int)(H / Hk);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    ScanArgs base{};
+    base.H = (int)H;
+    base.log_decay = log_decay;
+    base.qk_scale = scale;
+    base.bf16 = dtype == SSD_BF16;
+    base.batch = d->batch; base.L = d->seqlen; base.rows = rows;
+    base.cu = cu_seqlens;
+    if (!(base.err = device_error_flag())) return SSD_ERR_CUDA;
+    float* shared = group > 1 ? static_cast<float*>(workspace) : nullptr;
+
+    ScanArgs a = base;  // dq
+    a.q = d_o; a.rs_q = H * Dv; a.gq = 1;
+    a.k = v; a.rs_k = Hk * Dv; a.gk = group;
+    a.v = k; a.rs_v = Hk * Dk; a.gv = group;
+    a.Dk = (int)Dv; a.Dv = (int)Dk;
+    a.inter_scale = scale; a.w_scale = 1.f;
+    a.init = init_state; a.init_t = true;
+    a.o = dq;
+    cudaError_t e = launch_scan(a, cs);
+    if (e != cudaSuccess) return SSD_ERR_CUDA;
+
+    a = base;  // dk
+    a.reverse = true;
+    a.inter_scale = 1.f; a.w_scale = scale;
+    a.q = v; a.rs_q = Hk * Dv; a.gq = group;
+    a.k = d_o; a.rs_k = H * Dv; a.gk = 1;
+    a.v = q; a.rs_v = H * Dk; a.gv = 1;
+    a.Dk = (int)Dv; a.Dv = (int)Dk;
+    a.init = d_final_state; a.init_t = true;
+    a.o = shared ? shared : dk;
+    a.o_f32 = shared || dtype == SSD_F32;
+    e = launch_scan(a, cs);
+    if (e == cudaSuccess && shared) e = launch_group_sum(shared, dk, rows, (int)Hk, group, (int)Dk, base.bf16, cs);
+    if (e != cudaSuccess) return SSD_ERR_CUDA;
+
+    a = base;  // dv, and the initial state's gradient
+    a.reverse = true;
+    a.inter_scale = 1.f; a.w_scale = scale;
+    a.q = k; a.rs_q = Hk * Dk; a.gq = group;
+    a.k = q; a.rs_k = H * Dk; a.gk = 1;
+    a.v = d_o; a.rs_v = H * Dv; a.gv = 1;
+    a.Dk = (int)Dk; a.Dv = (int)Dv;
+    a.init = d_final_state;
+    a.final_state = d_init_state;
+    a.o = shared ? shared : dv;
+    a.o_f32 = shared || dtype == SSD_F32;
+    e = launch_scan(a, cs);
+    if (e == cudaSuccess && shared) e = launch_group_sum(shared, dv, rows, (int)Hk, group, (int)Dv, base.bf16, cs);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_linear_attn_decode_step(const ssd_linear_attn_dims* d, ssd_dtype dtype, const float* log_decay,
+                                       float scale, const void* q, const void* k, const void* v, float* state, void* o,
+                                       void* stream) {
+    if (!d) return SSD_ERR_NULL;
+    ssd_linear_attn_dims one = *d;
+    one.seqlen = 1;
+    const ssd_status st = la::check_dims(&one, dtype);
+    if (st != SSD_OK) return st;
+    if (!isfinite(scale)) return SSD_ERR_SHAPE;
+    if (!log_decay || (d->batch > 0 && (!q || !k || !v || !state || !o))) return SSD_ERR_NULL;
+    for (const void* p : {q, k, v, (const void*)state, (const void*)o})
+        if (!aligned16(p)) return SSD_ERR_ALIGN;
+    if (!offsets_aligned(log_decay, nullptr)) return SSD_ERR_ALIGN;
+    const uint64_t es = dtype == SSD_F32 ? 4 : 2, H = d->nheads, Hk = d->kv_heads, Dk = d->key_dim, Dv = d->value_dim;
+    const uint64_t b = d->batch;
+    const Buffer ins[] = {{q, b * H * Dk * es}, {k, b * Hk * Dk * es}, {v, b * Hk * Dv * es}, {log_decay, H * 4}};
+    const Buffer outs[] = {{state, b * H * Dk * Dv * 4}, {o, b * H * Dv * es}};
+    if (outputs_alias(outs, ins)) return SSD_ERR_UNSUPPORTED;
+    if (d->batch == 0) return SSD_OK;
+    la::DecodeArgs a{};
+    a.batch = d->batch;
+    a.H = (int)H; a.Hk = (int)Hk; a.Dk = (int)Dk; a.Dv = (int)Dv;
+    a.log_decay = log_decay;
+    a.scale = scale;
+    a.bf16 = dtype == SSD_BF16;
+    a.q = q; a.k = k; a.v = v;
+    a.state = state;
+    a.o = o;
+    return la::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -43,6 +43,24 @@ class SsdGrads(ctypes.Structure):
                                                "dconv_b", "d_init_state", "d_init_conv_state")]
 
 
+class SsdLinearAttnDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("key_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32)]
+
+
+class SsdLinearAttnStrides(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64), ("v", ctypes.c_int64)]
+
+
+class SsdQkDims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class SsdQkStrides(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
 class SsdError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {STATUS.get(status, status)} ({lib().ssd_status_string(status).decode()})")
@@ -104,6 +122,25 @@ def lib() -> ctypes.CDLL:
         L.ssd_test_stall_prefill.argtypes = [ctypes.c_uint64]
         L.ssd_set_timing_events.restype = ctypes.c_int
         L.ssd_set_timing_events.argtypes = [vp, vp]
+        lap, qkp = ctypes.POINTER(SsdLinearAttnDims), ctypes.POINTER(SsdQkDims)
+        L.ssd_linear_attn_prefill_workspace_bytes.restype = sz
+        L.ssd_linear_attn_prefill_workspace_bytes.argtypes = [lap, ctypes.c_int, ctypes.c_int]
+        L.ssd_linear_attn_prefill.restype = ctypes.c_int
+        L.ssd_linear_attn_prefill.argtypes = [lap, ctypes.c_int, vp, ctypes.c_float,
+                                              ctypes.POINTER(SsdLinearAttnStrides)] + [vp] * 8 + [sz, vp]
+        L.ssd_linear_attn_backward_workspace_bytes.restype = sz
+        L.ssd_linear_attn_backward_workspace_bytes.argtypes = [lap, ctypes.c_int, ctypes.c_int]
+        L.ssd_linear_attn_backward.restype = ctypes.c_int
+        L.ssd_linear_attn_backward.argtypes = [lap, ctypes.c_int, vp, ctypes.c_float] + [vp] * 12 + [sz, vp]
+        L.ssd_linear_attn_decode_step.restype = ctypes.c_int
+        L.ssd_linear_attn_decode_step.argtypes = [lap, ctypes.c_int, vp, ctypes.c_float] + [vp] * 6
+        L.ssd_qk_norm_rope.restype = ctypes.c_int
+        L.ssd_qk_norm_rope.argtypes = [qkp, ctypes.c_int, ctypes.c_float, ctypes.POINTER(SsdQkStrides)] + [vp] * 9
+        L.ssd_qk_norm_rope_backward_workspace_bytes.restype = sz
+        L.ssd_qk_norm_rope_backward_workspace_bytes.argtypes = [qkp]
+        L.ssd_qk_norm_rope_backward.restype = ctypes.c_int
+        L.ssd_qk_norm_rope_backward.argtypes = [qkp, ctypes.c_int, ctypes.c_float,
+                                                ctypes.POINTER(SsdQkStrides)] + [vp] * 13 + [sz, vp]
         _lib = L
     return _lib
 
@@ -540,6 +577,231 @@ def mimo_decode_step(x, dt, B, C, z, A, D, dt_bias, ssm_state, y=None, y_dtype=N
     if st != 0:
         raise SsdError(st, "ssd_mimo_decode_step")
     return y
+
+
+def _act_code(t, name="q") -> int:
+    if t.dtype == torch.bfloat16:
+        return SSD_BF16
+    if t.dtype == torch.float32:
+        return SSD_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _enqueue(what, dev, *args):
+    """Calls ``what`` with the current stream of ``dev`` (which need not be the current device)."""
+    fn = getattr(lib(), what)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream_ptr(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream_ptr(dev))
+    if st != 0:
+        raise SsdError(st, what)
+
+
+def _workspace(workspace, need, dev):
+    """A workspace of at least ``need`` bytes: the caller's if it is large enough, else a new one (or None)."""
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace, workspace.numel() * workspace.element_size()
+    if not need:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=dev), need
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+    return t.device
+
+
+def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved):
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise ValueError("q and k must be [T, heads, D] or [Bt, L, heads, D]")
+    dev = _cuda_device(q, "q")
+    lead, Hq, Hk, D = tuple(q.shape[:-2]), q.shape[-2], k.shape[-2], q.shape[-1]
+    rows = lead if len(lead) == 2 else (1,) + lead
+    rs = SsdQkStrides(*[_row_stride(t if len(lead) == 2 else t.unsqueeze(0), name, rows + (n, D), q.dtype, dev)
+                        for name, t, n in (("q", q, Hq), ("k", k, Hk))])
+    _check(q_weight, "q_weight", (D,), torch.float32, dev)
+    _check(k_weight, "k_weight", (D,), torch.float32, dev)
+    _check(positions, "positions", lead, torch.int64, dev)
+    half = inv_freq.numel()
+    _check(inv_freq, "inv_freq", (half,), torch.float32, dev)
+    dims = SsdQkDims(rows[0] * rows[1], Hq, Hk, D, 2 * half, int(bool(interleaved)))
+    return dev, dims, rs, _act_code(q)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
+    """RMSNorm of every query and key head and the rotation by position, in one pass.
+
+    q [..., Hq, D], k [..., Hk, D] with leading dimensions [T] or [Bt, L] (bf16 or fp32, contiguous or views with
+    strided rows, e.g. slices of a fused projection); q_weight, k_weight [D] fp32; positions, shaped as the
+    leading dimensions, int64; inv_freq [rot/2] fp32, rot <= D: the first rot channels of a head are turned by
+    positions * inv_freq (taken in fp64), in pairs (p, p + rot/2), or (2p, 2p + 1) with ``interleaved``.
+    Returns (q_out, k_out), contiguous; a contiguous input may be its own output.
+    """
+    dev, dims, rs, code = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    _check(q_out, "q_out", tuple(q.shape), q.dtype, dev)
+    _check(k_out, "k_out", tuple(k.shape), q.dtype, dev)
+    _enqueue("ssd_qk_norm_rope", dev, ctypes.byref(dims), code, float(eps), ctypes.byref(rs), _ptr(q), _ptr(k),
+             _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(q_out), _ptr(k_out))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False,
+                          workspace=None):
+    """Gradients of ``qk_norm_rope`` from those of its outputs (contiguous).  Returns a dict keyed by the input
+    they belong to: q, k (the activation dtype, contiguous), q_weight, k_weight (fp32)."""
+    dev, dims, rs, code = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
+    _check(dq_out, "dq_out", tuple(q.shape), q.dtype, dev)
+    _check(dk_out, "dk_out", tuple(k.shape), q.dtype, dev)
+    out = {"q": torch.empty(q.shape, dtype=q.dtype, device=dev), "k": torch.empty(k.shape, dtype=q.dtype, device=dev),
+           "q_weight": torch.empty_like(q_weight), "k_weight": torch.empty_like(k_weight)}
+    workspace, ws_bytes = _workspace(workspace, int(lib().ssd_qk_norm_rope_backward_workspace_bytes(
+        ctypes.byref(dims))), dev)
+    _enqueue("ssd_qk_norm_rope_backward", dev, ctypes.byref(dims), code, float(eps), ctypes.byref(rs), _ptr(dq_out),
+             _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+             _ptr(out["q"]), _ptr(out["k"]), _ptr(out["q_weight"]), _ptr(out["k_weight"]), _ptr(workspace), ws_bytes)
+    return out
+
+
+def _offsets(cu_seqlens, dev):
+    """Packed-sequence offsets as a device tensor, and the number of sequences."""
+    if not torch.is_tensor(cu_seqlens) or cu_seqlens.device != dev:
+        cu_seqlens = torch.as_tensor(cu_seqlens, dtype=torch.int64).to(dev)
+    if cu_seqlens.dtype != torch.int64 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous 1-D int64 tensor")
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens needs at least one entry")
+    return cu_seqlens, cu_seqlens.numel() - 1
+
+
+def _linear_attn_prefill(q, k, v, log_decay, cu_seqlens, init_state, scale, workspace, o, final_state):
+    dev = _cuda_device(q, "q")
+    packed = cu_seqlens is not None
+    if packed:
+        cu_seqlens, Bt = _offsets(cu_seqlens, dev)
+        rows = (1, q.shape[0])
+    else:
+        Bt = q.shape[0]
+        rows = tuple(q.shape[:2])
+    H, Dk, Hk, Dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    rs = SsdLinearAttnStrides(*[_row_stride(t.unsqueeze(0) if packed else t, name, rows + tail, q.dtype, dev)
+                                for name, t, tail in (("q", q, (H, Dk)), ("k", k, (Hk, Dk)), ("v", v, (Hk, Dv)))])
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    state = (Bt, H, Dk, Dv)
+    if init_state is not None:
+        _check(init_state, "init_state", state, torch.float32, dev)
+    if o is None:
+        o = torch.empty(tuple(q.shape[:-1]) + (Dv,), dtype=q.dtype, device=dev)
+    if final_state is None:
+        final_state = torch.empty(state, dtype=torch.float32, device=dev)
+    _check(o, "o", tuple(q.shape[:-1]) + (Dv,), q.dtype, dev)
+    _check(final_state, "final_state", state, torch.float32, dev)
+    dims = SsdLinearAttnDims(Bt, rows[1], H, Hk, Dk, Dv)
+    code = _act_code(q)
+    need = int(lib().ssd_linear_attn_prefill_workspace_bytes(ctypes.byref(dims), code, int(packed)))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    _enqueue("ssd_linear_attn_prefill", dev, ctypes.byref(dims), code, _ptr(log_decay),
+             float(Dk ** -0.5 if scale is None else scale), ctypes.byref(rs), _ptr(cu_seqlens), _ptr(q), _ptr(k),
+             _ptr(v), _ptr(init_state), _ptr(o), _ptr(final_state), _ptr(workspace), ws_bytes)
+    return o, final_state
+
+
+def linear_attn_prefill(q, k, v, log_decay, init_state=None, scale=None, workspace=None, o=None, final_state=None):
+    """Decayed linear attention over prompts: S_t = e^log_decay S_{t-1} + k_t v_t^T, o_t = scale q_t S_t.
+
+    q [Bt, L, H, Dk], k [Bt, L, Hk, Dk], v [Bt, L, Hk, Dv] (bf16 or fp32, one dtype; H a multiple of Hk),
+    contiguous or views with strided rows; log_decay [H] fp32, <= 0, a constant of the layer; init_state
+    [Bt, H, Dk, Dv] fp32 or None; scale: Dk ** -0.5 by default.  Dk and Dv are multiples of 8 up to 128.
+    Returns (o [Bt, L, H, Dv], final_state [Bt, H, Dk, Dv] fp32); final_state may be init_state's tensor.
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be [Bt, L, H, Dk]")
+    return _linear_attn_prefill(q, k, v, log_decay, None, init_state, scale, workspace, o, final_state)
+
+
+def linear_attn_prefill_varlen(q, k, v, log_decay, cu_seqlens, init_state=None, scale=None, workspace=None, o=None,
+                               final_state=None):
+    """``linear_attn_prefill`` on a packed batch: sequence s is rows cu_seqlens[s] .. cu_seqlens[s+1]-1.
+
+    q [T, H, Dk], k [T, Hk, Dk], v [T, Hk, Dv]; cu_seqlens: nseq+1 non-decreasing offsets, an int64 tensor on
+    the device (a list or CPU tensor is copied there first); init_state [nseq, H, Dk, Dv] fp32 or None.
+    Returns (o [T, H, Dv], final_state [nseq, H, Dk, Dv]); rows outside every sequence are not written.
+    Offsets that are out of order or out of range are reported by device_status().
+    """
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, Dk]")
+    return _linear_attn_prefill(q, k, v, log_decay, cu_seqlens, init_state, scale, workspace, o, final_state)
+
+
+def linear_attn_backward(q, k, v, log_decay, do, init_state=None, d_final_state=None, scale=None, cu_seqlens=None,
+                         want_init_grads=True, workspace=None):
+    """Gradients of ``linear_attn_prefill`` (or, with ``cu_seqlens``, of ``linear_attn_prefill_varlen``).
+
+    Inputs as for the forward (contiguous); do is shaped as o, d_final_state as final_state, or None.
+    Returns a dict keyed by the input they belong to: q, k, v (the activation dtype) and, with
+    ``want_init_grads``, init_state (fp32): the gradients of sum(do * o) + sum(d_final_state * final_state).
+    """
+    dev = _cuda_device(q, "q")
+    packed = cu_seqlens is not None
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("q must be [T, H, Dk] with cu_seqlens, else [Bt, L, H, Dk]")
+    if packed:
+        cu_seqlens, Bt = _offsets(cu_seqlens, dev)
+    else:
+        Bt = q.shape[0]
+    lead = tuple(q.shape[:-2])
+    H, Dk, Hk, Dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
+    for name, t, tail in (("q", q, (H, Dk)), ("k", k, (Hk, Dk)), ("v", v, (Hk, Dv)), ("do", do, (H, Dv))):
+        _check(t, name, lead + tail, q.dtype, dev)
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    state = (Bt, H, Dk, Dv)
+    if init_state is not None:
+        _check(init_state, "init_state", state, torch.float32, dev)
+    if d_final_state is not None:
+        _check(d_final_state, "d_final_state", state, torch.float32, dev)
+    out = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+    if want_init_grads:
+        out["init_state"] = torch.empty(state, dtype=torch.float32, device=dev)
+    dims = SsdLinearAttnDims(Bt, lead[-1], H, Hk, Dk, Dv)
+    code = _act_code(q)
+    need = int(lib().ssd_linear_attn_backward_workspace_bytes(ctypes.byref(dims), code, int(packed)))
+    workspace, ws_bytes = _workspace(workspace, need, dev)
+    _enqueue("ssd_linear_attn_backward", dev, ctypes.byref(dims), code, _ptr(log_decay),
+             float(Dk ** -0.5 if scale is None else scale), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
+             _ptr(init_state), _ptr(do), _ptr(d_final_state), _ptr(out["q"]), _ptr(out["k"]), _ptr(out["v"]),
+             _ptr(out.get("init_state")), _ptr(workspace), ws_bytes)
+    return out
+
+
+def linear_attn_decode_step(q, k, v, log_decay, state, scale=None, o=None):
+    """One token of decayed linear attention for Bt sequences; ``state`` updates in place.
+
+    q [Bt, H, Dk], k [Bt, Hk, Dk], v [Bt, Hk, Dv] (bf16 or fp32); log_decay [H] fp32; state [Bt, H, Dk, Dv] fp32.
+    Returns o [Bt, H, Dv].
+    """
+    dev = _cuda_device(q, "q")
+    Bt, H, Dk = q.shape
+    Hk, Dv = k.shape[1], v.shape[2]
+    for name, t, shp in (("q", q, (Bt, H, Dk)), ("k", k, (Bt, Hk, Dk)), ("v", v, (Bt, Hk, Dv))):
+        _check(t, name, shp, q.dtype, dev)
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    _check(state, "state", (Bt, H, Dk, Dv), torch.float32, dev)
+    if o is None:
+        o = torch.empty((Bt, H, Dv), dtype=q.dtype, device=dev)
+    _check(o, "o", (Bt, H, Dv), q.dtype, dev)
+    dims = SsdLinearAttnDims(Bt, 1, H, Hk, Dk, Dv)
+    _enqueue("ssd_linear_attn_decode_step", dev, ctypes.byref(dims), _act_code(q), _ptr(log_decay),
+             float(Dk ** -0.5 if scale is None else scale), _ptr(q), _ptr(k), _ptr(v), _ptr(state), _ptr(o))
+    return o
 
 
 def device_status(device="cuda"):
