@@ -181,7 +181,7 @@ ssd_status check_dims(const ssd_linear_attn_dims* d, ssd_dtype dtype) {
     if (d->nheads <= 0 || d->kv_heads <= 0 || d->nheads % d->kv_heads != 0 || d->nheads > 65535) return SSD_ERR_SHAPE;
     for (int w : {d->key_dim, d->value_dim})
         if (w < 8 || w > 128 || w % 8 != 0) return SSD_ERR_SHAPE;
-    if (d->batch > (1LL << 31) - 1 || d->batch * (int64_t)d->nheads > (1LL << 31) - 1) return SSD_ERR_SHAPE;
+    if (d->batch > (1LL << 31) - 1 || d->batch * (int64_t)d->nheads > (1LL << 30) - 1) return SSD_ERR_SHAPE;
     return SSD_OK;
 }
 
@@ -217,7 +217,9 @@ template <int NO, int NI> bool outputs_alias(const Buffer (&outs)[NO], const Buf
 }
 
 // One scan: whole sequences.
-cudaError_t launch_scan(ScanArgs a, cudaStream_t st) { return launch_scan_simt(a, kWhole, st); }
+cudaError_t launch_scan(ScanArgs a, cudaStream_t st) {
+    return a.bf16 ? launch_scan_tc(a, kWhole, st) : launch_scan_simt(a, kWhole, st);
+}
 
 }  // namespace
 }  // namespace la

@@ -100,6 +100,8 @@ __device__ __forceinline__ float decay_pow(float l, int64_t n) { return n == 0 ?
 
 // CUDA-core scan.
 cudaError_t launch_scan_simt(const ScanArgs& a, Mode mode, cudaStream_t st);
+// Tensor-core scan (bf16 rows).
+cudaError_t launch_scan_tc(const ScanArgs& a, Mode mode, cudaStream_t st);
 
 // Runs the segments' states into one another: seg_state[i] becomes the state before segment i (in scan
 // order, from init), final_state the state behind the last one.

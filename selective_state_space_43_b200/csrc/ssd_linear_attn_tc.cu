@@ -1,0 +1,484 @@
+// ssd_linear_attn_tc.cu -- decayed linear attention on the sm_100a tensor cores (bf16 rows).
+//
+// One CTA per (64 value channels, head, sequence or segment) walks its rows in chunks of C = 128:
+//   P  = (Q K^T) . D,  D_ij = qk_scale e^{l(i-j)} for j <= i, else 0      [C x C]    tcgen05, K = Dk
+//   Y1 = P V                                                              [C x 64]   tcgen05, K = C
+//   Y2 = Q S                                                              [C x 64]   tcgen05, K = Dk
+//   dS = K^T V',  V'_j = w_scale e^{l(C-j-s)} v_j                         [Dk x 64]  tcgen05, K = C
+//   o_i = Y1_i + inter_scale e^{l(i+s)} Y2_i,   S <- e^{lC} S + dS
+// (rows i counted in time order; against the time the tile's rows are counted from its end and the mask is
+// the upper triangle).  Widths below 128 run in the same tiles: the tensor maps fill with zeros.
+//
+// Because the decay is a constant of the head, D, w and the output coefficients are the same for every chunk:
+// each thread computes its 64 mask entries, its row weight and its coefficient once and keeps them in
+// registers, so a score costs one multiply and half a conversion.  The state S is held in fp32 in the
+// registers of one warpgroup (a key row of 64 channels per thread), dS is computed from zero each chunk: no
+// accumulator is carried through the tensor cores, and nothing but that warpgroup's multiply-adds depends on the
+// chunk before.
+//
+// Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself
+// stays fp32); o once.  V' is split into kTerms bf16 parts (v w = hi + mid + lo, each the rounding of what the parts
+// before leave): 3 parts carry 24 bits, so a state that the caller gets is as exact as fp32 sums; 2 parts
+// (17 bits) where S only feeds bf16 outputs.
+//
+// 18 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
+//   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
+//   8-11  V' of the next chunk (shared memory -> shared memory), then S of this one (TMEM -> registers ->
+//         shared memory); the same threads zero the rows behind a sequence's end in K and V
+//   12-15 o: TMEM -> global
+//   16    TMA: Q, K, V of a chunk, two stages
+//   17    tcgen05.mma
+// Bound by HBM where there are enough heads: Q, K, V are read once (Q and K once for each 64 value
+// channels, the second time from L2), o written once.
+#include "ssd_common.cuh"
+#include "ssd_internal.h"
+#include "ssd_linear_attn.h"
+#include "ssd_sm100.cuh"
+
+extern __shared__ __align__(1024) unsigned char ssd_la_smem[];
+
+namespace ssd {
+namespace la {
+namespace {
+
+using namespace ssd::sm100;
+
+constexpr int C = 128, DVB = 64;
+constexpr int kWarpTma = 16, kWarpMma = 17, kThreads = 18 * 32;
+constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
+constexpr uint32_t kStage = 5 * kBox;            // Q (2), K (2), V (1)
+constexpr uint32_t OFF_K = 2 * kBox, OFF_V = 4 * kBox;
+constexpr uint32_t OFF_VP = 2 * kStage;          // V': up to three boxes
+constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
+constexpr uint32_t OFF_BAR = OFF_S + kBox;
+constexpr uint32_t kSmemBytes = OFF_BAR + 256 + 1024;  // + alignment of the base
+enum Bar { FULL = 0, EMPTY = 2, PFULL = 4, PREADY = 6, VREADY = 8, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, kBars };
+// TMEM columns: scores (two buffers; their bf16 form overlays each half), Y1, Y2, dS (two buffers)
+constexpr uint32_t COL_P = 0, COL_Y1 = 256, COL_Y2 = 320, COL_DS = 384;
+
+struct Params {
+    CUtensorMap tq, tk, tv;
+    ScanArgs a;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: the A operand's rows are TMEM lanes, two bf16 to a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// kMode: see Mode.  kTerms: bf16 parts of V'.  TO: type of the outputs.
+template <int kMode, int kTerms, typename TO>
+__global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ Params prm) {
+    const ScanArgs& a = prm.a;
+    uint8_t* sm = ssd_la_smem + ((1024u - (smem_u32(ssd_la_smem) & 1023u)) & 1023u);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
+    volatile int* stop = reinterpret_cast<volatile int*>(sm + OFF_BAR + 200);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_BAR + 208);
+    constexpr bool kOut = kMode != kStates;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ndvb = (a.Dv + DVB - 1) / DVB;
+    const int dv0 = (int)(blockIdx.x % ndvb) * DVB;
+    const int h = (int)(blockIdx.x / ndvb % a.H);
+    const int64_t slot = blockIdx.x / ((unsigned)ndvb * a.H);
+    const Segment g = segment_of(a, slot);
+    if (a.cu && a.seg_len == 0 && tid == 0 && h == 0 && dv0 == 0 && !sequence_span(a, slot).ok)
+        atomicOr(a.err, kErrBadSeqlens);
+    if (!g.ok) return;
+    const int nv = min(DVB, a.Dv - dv0);
+    const int nc = (int)((g.n + C - 1) / C);
+    const bool rev = a.reverse;
+    // chunk c in scan order -> its first row and its rows
+    auto chunk_row = [&](int c) { return g.row0 + (int64_t)(rev ? nc - 1 - c : c) * C; };
+    auto chunk_n = [&](int c) {
+        const int64_t left = g.n - (int64_t)(rev ? nc - 1 - c : c) * C;
+        return left < C ? (int)left : C;
+    };
+
+    if (warp == kWarpMma) {
+        if (lane == 0) {
+            for (int i = 0; i < kBars; ++i)
+                mbar_init(&bars[i], (i == PREADY || i == PREADY + 1) ? 8
+                                    : i == VREADY || i == SREADY || i == EPI ? 4
+                                                                             : 1);
+            *stop = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const float l = a.log_decay[h];
+    const int ksteps = a.Dk > 64 ? 8 : 4;
+    const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
+    const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
+
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            int last0 = -1, last1 = -1;  // last chunk loaded into each stage
+            const int boxes = a.Dk > 64 ? 2 : 1;
+            for (int c = 0; c < nc; ++c) {
+                const int s = c & 1;
+                if (c >= 2 && !mbar_wait(&bars[EMPTY + s], ((c >> 1) - 1) & 1, stop)) { *stop = 1; break; }
+                uint8_t* st = sm + s * kStage;
+                const int r = (int)chunk_row(c);
+                mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
+                for (int b = 0; b < boxes; ++b) {
+                    tma_load_3d(st + OFF_K + b * kBox, &prm.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                    if (kOut) tma_load_3d(st + b * kBox, &prm.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                }
+                tma_load_3d(st + OFF_V, &prm.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                if (s) last1 = c;
+                else last0 = c;
+            }
+            // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
+            if (last0 >= 0) mbar_wait(&bars[FULL], (last0 >> 1) & 1, nullptr, 100000000ull);
+            if (last1 >= 0) mbar_wait(&bars[FULL + 1], (last1 >> 1) & 1, nullptr, 100000000ull);
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            constexpr uint32_t ID_P = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t ID_Y = idesc_bf16_f32(128, 64, false, true);
+            constexpr uint32_t ID_DS = idesc_bf16_f32(128, 64, true, true);
+            const uint32_t base = smem_u32(sm);
+            const uint64_t dVP = sw128_desc(base + OFF_VP, 16384, 1024), dS = sw128_desc(base + OFF_S, 16384, 1024);
+            auto scores = [&](int c) {  // P(c) = Q K^T
+                const uint32_t st = base + (c & 1) * kStage;
+                const uint64_t dQ = sw128_desc(st, 16, 1024), dK = sw128_desc(st + OFF_K, 16, 1024);
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                    mma_bf16(tmem + COL_P + (c & 1) * 128, dQ + o, dK + o, ID_P, k > 0);
+                }
+                mma_commit(&bars[PFULL + (c & 1)]);
+            };
+            int issued = 0;  // chunks whose scores are under way
+            for (int c = 0; c < nc; ++c) {
+                const int s = c & 1;
+                const uint32_t st = base + s * kStage;
+                if (kOut && issued <= c) {
+                    if (!mbar_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                    tc_fence_after();
+                    scores(c);
+                    issued = c + 1;
+                }
+                // dS(c) = K^T V' (V' is written after the tiles have landed)
+                if (!mbar_wait(&bars[VREADY], c & 1, stop)) { *stop = 1; break; }
+                tc_fence_after();
+                const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024);
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16(tmem + COL_DS + s * 64, dKt + k * 128, dVP + ((t * kBox) >> 4) + k * 128, ID_DS,
+                                 t > 0 || k > 0);
+                mma_commit(&bars[DSFULL]);
+                if (kOut) {
+                    // Y2(c) = Q S, once S is written and the chunk before has been read out
+                    if (!mbar_wait(&bars[SREADY], c & 1, stop) || (c >= 1 && !mbar_wait(&bars[EPI], (c - 1) & 1, stop))) {
+                        *stop = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dQ = sw128_desc(st, 16, 1024);
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_bf16(tmem + COL_Y2, dQ + (((k >> 2) * kBox + (k & 3) * 32) >> 4), dS + k * 128, ID_Y, k > 0);
+                    mma_commit(&bars[Y2DONE]);
+                    // the next chunk's scores, if its tiles are here already (never waited for: this chunk's
+                    // stage has to be freed for the load behind it)
+                    if (c + 1 < nc && mbar_try_wait(&bars[FULL + (s ^ 1)], ((c + 1) >> 1) & 1)) {
+                        tc_fence_after();
+                        scores(c + 1);
+                        issued = c + 2;
+                    }
+                    // Y1(c) = P V
+                    if (!mbar_wait(&bars[PREADY + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                    tc_fence_after();
+                    const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
+                        mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + s * 128 + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128,
+                                    ID_Y, k > 0);
+                    mma_commit(&bars[YFULL]);
+                }
+                mma_commit(&bars[EMPTY + s]);
+            }
+            // nothing may still be running on the tensor cores when TMEM is released
+            mma_commit(&bars[MMADONE]);
+            mbar_wait(&bars[MMADONE], 0, nullptr, 100000000ull);
+        }
+    } else if (warp < 8) {
+        if (kOut) {
+            // ---- scores: row `row`, columns 64 half .. 64 half + 63 ----
+            const int j0 = (warp >> 2) * 64;
+            float m[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+                const int far = rev ? j0 + j - row : row - (j0 + j);
+                m[j] = far < 0 ? 0.f : far == 0 ? a.qk_scale : a.qk_scale * expf(l * (float)far);
+            }
+            for (int c = 0; c < nc; ++c) {
+                const int s = c & 1, n = chunk_n(c);
+                if (!warp_wait(&bars[PFULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                tc_fence_after();
+                const uint32_t col = lane_base + COL_P + s * 128 + j0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float v[16];
+                    uint32_t p[8];
+                    tmem_ld16(col + b * 16, v);
+                    tmem_wait_ld();
+                    if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = j0 + b * 16 + j < n ? v[j] : 0.f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] = pack_bf2(v[2 * j] * m[b * 16 + 2 * j], v[2 * j + 1] * m[b * 16 + 2 * j + 1]);
+                    tmem_st8(col + b * 8, p);  // over columns already read
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bars[PREADY + s], lane);
+            }
+        }
+    } else if (warp < 12) {
+        // ---- V' and S: tile row / key row `row` ----
+        float S[DVB];
+        const size_t size = (size_t)a.Dk * a.Dv;
+        const float* init = kMode == kOutputs ? a.seg_state + ((size_t)slot * a.H + h) * size
+                            : kMode == kStates || !a.init ? nullptr
+                                                          : a.init + ((size_t)g.seq * a.H + h) * size;
+        const bool init_t = kMode == kWhole && a.init_t;
+#pragma unroll
+        for (int d = 0; d < DVB; ++d)
+            S[d] = init && row < a.Dk && d < nv
+                       ? init[init_t ? (size_t)(dv0 + d) * a.Dk + row : (size_t)row * a.Dv + dv0 + d]
+                       : 0.f;
+        auto publish = [&] {  // the bf16 copy that Y2 reads
+            uint8_t* p = sm + OFF_S;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(p + sw128_off(row, i)) =
+                    make_uint4(pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
+                               pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
+            fence_async_smem();
+            warp_arrive(&bars[SREADY], lane);
+        };
+        auto weight = [&](int n) {  // of tile row `row` in the state behind a chunk of n rows
+            return a.w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row);
+        };
+        const float w_full = weight(C), decay_full = decay_pow(l, C);
+        auto split = [&](int c) {  // V'(c), and zeros behind the sequence's end
+            const int n = chunk_n(c);
+            uint8_t* st = sm + (c & 1) * kStage;
+            const float w = n == C ? w_full : row < n ? weight(n) : 0.f;
+            if (row >= n) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t o = sw128_off(row, i);
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(st + OFF_K + o) = z;
+                    *reinterpret_cast<uint4*>(st + OFF_K + kBox + o) = z;
+                    *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t o = sw128_off(row, i);
+                const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
+                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                uint32_t part[kTerms][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float f0 = bf_lo(in[k]) * w, f1 = bf_hi(in[k]) * w;
+#pragma unroll
+                    for (int t = 0; t < kTerms; ++t) {
+                        part[t][k] = pack_bf2(f0, f1);
+                        f0 -= bf_lo(part[t][k]);
+                        f1 -= bf_hi(part[t][k]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+                    *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
+                        make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
+            }
+            fence_async_smem();
+            warp_arrive(&bars[VREADY], lane);
+        };
+        bool ok = true;
+        if (nc > 0) {
+            if (kOut) publish();
+            ok = warp_wait(&bars[FULL], 0, stop);
+            if (ok) split(0);
+        }
+        for (int c = 0; ok && c < nc; ++c) {
+            ok = warp_wait(&bars[DSFULL], c & 1, stop);
+            if (!ok) break;
+            if (c + 1 < nc) {  // the next V' first: its product runs while S is updated
+                ok = warp_wait(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1, stop);
+                if (!ok) break;
+                split(c + 1);
+            }
+            tc_fence_after();
+            const int n = chunk_n(c);
+            const float e = n == C ? decay_full : decay_pow(l, n);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float v[16];
+                tmem_ld16(lane_base + COL_DS + (c & 1) * 64 + b * 16, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) S[b * 16 + j] = fmaf(e, S[b * 16 + j], v[j]);
+            }
+            tc_fence_before();
+            if (kOut && c + 1 < nc) {
+                ok = warp_wait(&bars[Y2DONE], c & 1, stop);
+                if (!ok) break;
+                publish();
+            }
+        }
+        if (!ok) *stop = 1;
+        float* fin = kMode == kStates  ? a.seg_state + ((size_t)slot * a.H + h) * size
+                     : kMode == kWhole ? (a.final_state ? a.final_state + ((size_t)g.seq * a.H + h) * size : nullptr)
+                                       : nullptr;
+        if (ok && fin && row < a.Dk) {
+            float* p = fin + (size_t)row * a.Dv + dv0;
+#pragma unroll
+            for (int d = 0; d < DVB; d += 4)
+                if (d < nv) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
+        }
+    } else if (warp < 16) {
+        if (kOut) {
+            // ---- outputs: tile row `row` ----
+            auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
+            const float e_full = coefficient(C);
+            for (int c = 0; c < nc; ++c) {
+                const int n = chunk_n(c);
+                const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
+                if (!warp_wait(&bars[YFULL], c & 1, stop)) { *stop = 1; break; }
+                tc_fence_after();
+                float o[DVB];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float x[16], y[16];
+                    tmem_ld16(lane_base + COL_Y1 + b * 16, x);
+                    tmem_ld16(lane_base + COL_Y2 + b * 16, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[b * 16 + j] = fmaf(e, y[j], x[j]);
+                }
+                tc_fence_before();
+                warp_arrive(&bars[EPI], lane);
+                if (row < n) {
+                    TO* dst = static_cast<TO*>(a.o) + (chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0;
+#pragma unroll
+                    for (int d = 0; d < DVB; d += 8) {
+                        if (d < nv) {
+                            if constexpr (sizeof(TO) == 2) {
+                                *reinterpret_cast<uint4*>(dst + d) =
+                                    make_uint4(pack_bf2(o[d], o[d + 1]), pack_bf2(o[d + 2], o[d + 3]),
+                                               pack_bf2(o[d + 4], o[d + 5]), pack_bf2(o[d + 6], o[d + 7]));
+                            } else {
+                                *reinterpret_cast<float4*>(dst + d) = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+                                *reinterpret_cast<float4*>(dst + d + 4) =
+                                    make_float4(o[d + 4], o[d + 5], o[d + 6], o[d + 7]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *stop) atomicOr(a.err, kErrTimeout);
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<EncodeTiledFn>(p)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+// Rows of one role: [rows][heads][width] with rows `stride` elements apart; boxes of 128 rows x 64 channels of a
+// head, 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* m, const void* base, int width, int heads, int64_t rows, int64_t stride) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kMode, int kTerms, typename TO> cudaError_t launch(const Params& prm, cudaStream_t st) {
+    static const cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kMode, kTerms, TO>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const ScanArgs& a = prm.a;
+    const int64_t blocks = (a.seg_len ? a.slots : a.batch) * a.H * ((a.Dv + DVB - 1) / DVB);
+    scan_tc_kernel<kMode, kTerms, TO><<<(unsigned)blocks, kThreads, kSmemBytes, st>>>(prm);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_scan_tc(const ScanArgs& a, Mode mode, cudaStream_t st) {
+    Params prm;
+    prm.a = a;
+    if (a.rows > 0 && (!make_map(&prm.tk, a.k, a.Dk, a.H / a.gk, a.rows, a.rs_k) ||
+                       !make_map(&prm.tv, a.v, a.Dv, a.H / a.gv, a.rows, a.rs_v) ||
+                       !make_map(&prm.tq, a.q, a.Dk, a.H / a.gq, a.rows, a.rs_q)))
+        return cudaErrorInvalidValue;
+    using bf16 = __nv_bfloat16;
+    if (mode == kStates) return launch<kStates, 3, bf16>(prm, st);
+    if (mode == kOutputs) return a.o_f32 ? launch<kOutputs, 2, float>(prm, st) : launch<kOutputs, 2, bf16>(prm, st);
+    if (a.final_state) return a.o_f32 ? launch<kWhole, 3, float>(prm, st) : launch<kWhole, 3, bf16>(prm, st);
+    return a.o_f32 ? launch<kWhole, 2, float>(prm, st) : launch<kWhole, 2, bf16>(prm, st);
+}
+
+}  // namespace la
+}  // namespace ssd

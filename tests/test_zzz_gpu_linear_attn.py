@@ -266,7 +266,8 @@ def test_bad_offsets_are_reported(dtype):
             ops.device_status()
         ops.device_status()  # reading clears it
         if cu[1] == 100 and cu[0] == 0:
-            assert torch.equal(o[:100], good[0][:100]) and torch.equal(S[0], good[1][0])
+            # the valid sequences are computed; rows 90 .. 99 belong to two of them in the first list
+            assert torch.equal(o[:90], good[0][:90]) and torch.equal(S[0], good[1][0])
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
