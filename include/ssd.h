@@ -433,7 +433,7 @@ typedef struct {
  *   strides     row strides of q, k, v, or NULL for contiguous rows
  *   cu_seqlens  device offsets of a packed batch, or NULL
  *   init_state  [batch][H][Dk][Dv] fp32 or NULL for zeros; may equal final_state
- *   o           [batch][seqlen][H][Dv] dtype (out), 32-byte aligned
+ *   o           [batch][seqlen][H][Dv] dtype (out)
  *   final_state [batch][H][Dk][Dv] fp32 (out): the state after each sequence's last token
  *   workspace   ssd_linear_attn_prefill_workspace_bytes() bytes (may be NULL when that is 0);
  *               two calls that may run at once need one each
@@ -447,7 +447,7 @@ SSD_API ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* dims, ssd
 
 /*
  * Gradients of the chunked form: of sum(d_o * o) + sum(d_final_state * final_state).
- * q, k, v, d_o contiguous; dq, dk, dv (out) laid out as q, k, v in dtype, 32-byte aligned (shared key
+ * q, k, v, d_o contiguous; dq, dk, dv (out) laid out as q, k, v in dtype (shared key
  * and value heads: the sum over their query heads, taken in fp32).  init_state and d_final_state may be
  * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.
  */

@@ -248,9 +248,10 @@ ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* d, ssd_dtype dtyp
     if (!isfinite(scale)) return SSD_ERR_SHAPE;
     if (!log_decay || (d->batch > 0 && !final_state)) return SSD_ERR_NULL;
     if (d->batch > 0 && rows > 0 && (!q || !k || !v || !o)) return SSD_ERR_NULL;
-    for (const void* p : {q, k, v, (const void*)init_state, (const void*)final_state, (const void*)workspace})
+    for (const void* p : {q, k, v, (const void*)o, (const void*)init_state, (const void*)final_state,
+                          (const void*)workspace})
         if (!aligned16(p)) return SSD_ERR_ALIGN;
-    if ((reinterpret_cast<uintptr_t>(o) & 31u) || !offsets_aligned(log_decay, cu_seqlens)) return SSD_ERR_ALIGN;
+    if (!offsets_aligned(log_decay, cu_seqlens)) return SSD_ERR_ALIGN;
     const int64_t H = d->nheads, Hk = d->kv_heads, Dk = d->key_dim, Dv = d->value_dim;
     const uint64_t es = dtype == SSD_F32 ? 4 : 2;
     ssd_linear_attn_strides rs{H * Dk, Hk * Dk, Hk * Dv};
@@ -316,11 +317,9 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dty
     if (!isfinite(scale)) return SSD_ERR_SHAPE;
     if (!log_decay) return SSD_ERR_NULL;
     if (d->batch > 0 && rows > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)) return SSD_ERR_NULL;
-    for (const void* p : {q, k, v, d_o, (const void*)init_state, (const void*)d_final_state, (const void*)d_init_state,
-                          (const void*)workspace})
+    for (const void* p : {q, k, v, d_o, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)init_state,
+                          (const void*)d_final_state, (const void*)d_init_state, (const void*)workspace})
         if (!aligned16(p)) return SSD_ERR_ALIGN;
-    for (const void* p : {dq, dk, dv})
-        if (reinterpret_cast<uintptr_t>(p) & 31u) return SSD_ERR_ALIGN;
     if (!offsets_aligned(log_decay, cu_seqlens)) return SSD_ERR_ALIGN;
     const int64_t H = d->nheads, Hk = d->kv_heads, Dk = d->key_dim, Dv = d->value_dim;
     const uint64_t es = dtype == SSD_F32 ? 4 : 2, n = (uint64_t)rows;

@@ -12,7 +12,7 @@
 // Because the decay is a constant of the head, D, w and the output coefficients are the same for every chunk:
 // each thread computes its 64 mask entries, its row weight and its coefficient once and keeps them in
 // registers, so a score costs one multiply and half a conversion.  The state S is held in fp32 in the
-// registers of one warpgroup (a key row of 64 channels per thread), dS is computed from zero each chunk: no
+// registers of one warpgroup (32 channels of a key row per thread), dS is computed from zero each chunk: no
 // accumulator is carried through the tensor cores, and nothing but that warpgroup's multiply-adds depends on the
 // chunk before.
 //
@@ -21,13 +21,13 @@
 // before leave): 3 parts carry 24 bits, so a state that the caller gets is as exact as fp32 sums; 2 parts
 // (17 bits) where S only feeds bf16 outputs.
 //
-// 18 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
+// 24 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
-//   8-11  V' of the next chunk (shared memory -> shared memory), then S of this one (TMEM -> registers ->
-//         shared memory); the same threads zero the rows behind a sequence's end in K and V
-//   12-15 o: TMEM -> global
-//   16    TMA: Q, K, V of a chunk, two stages
-//   17    tcgen05.mma
+//   8-15  V' of the next chunk (shared memory -> shared memory), then S of this one (TMEM -> registers ->
+//         shared memory), 32 channels each; the same threads zero the rows behind a sequence's end in K and V
+//   16-19 o: TMEM -> registers -> global, a row per thread in 32-byte stores
+//   20    TMA: Q, K, V of a chunk, two stages
+//   21    tcgen05.mma (22 and 23 only complete the warpgroup)
 // Bound by HBM where there are enough heads: Q, K, V are read once (Q and K once for each 64 value
 // channels, the second time from L2), o written once.
 #include "ssd_common.cuh"
@@ -43,8 +43,8 @@ namespace {
 
 using namespace ssd::sm100;
 
-constexpr int C = 128, DVB = 64;
-constexpr int kWarpTma = 16, kWarpMma = 17, kThreads = 18 * 32;
+constexpr int C = 128, DVB = 64, kHalf = 32;
+constexpr int kWarpOut = 16, kWarpTma = 20, kWarpMma = 21, kThreads = 24 * 32;
 constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
 constexpr uint32_t kStage = 5 * kBox;            // Q (2), K (2), V (1)
 constexpr uint32_t OFF_K = 2 * kBox, OFF_V = 4 * kBox;
@@ -61,8 +61,28 @@ struct Params {
     ScanArgs a;
 };
 
+// Moves registers between warpgroups: of the 768 x 80 launched with, 2 x 128 x 24 go to the scores, given by
+// V' and S (2 x 128 x 8), the outputs (128 x 8) and the last warpgroup (128 x 24).
+template <int N> __device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop));
+}
+// Whether the phase is complete, without waiting (try_wait suspends the thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     __syncwarp();
@@ -78,14 +98,62 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// D (+)= A B over K = 64: a K-major A of one 64-wide box, B alike or (kBmn) MN-major with 128-byte rows.
+template <bool kBmn>
+__device__ __forceinline__ void mma_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) mma_bf16(d, a + k * 2, b + k * (kBmn ? 128 : 2), idesc, accumulate || k > 0);
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {  // 32-byte aligned
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Stores the first `n` (a multiple of 8, or none) of 16 channels.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16], int n, bool wide) {
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = pack_bf2(v[2 * j], v[2 * j + 1]);
+    if (wide && n >= 16) {
+        store32(p, r);
+    } else {
+        if (n >= 8) *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+        if (n >= 16) *reinterpret_cast<uint4*>(p + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[16], int n, bool wide) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(v[8 * b + j]);
+        if (n < 8 * b + 8) break;
+        if (wide) {
+            store32(p + 8 * b, r);
+        } else {
+            *reinterpret_cast<uint4*>(p + 8 * b) = make_uint4(r[0], r[1], r[2], r[3]);
+            *reinterpret_cast<uint4*>(p + 8 * b + 4) = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+    }
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -100,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_BAR + 208);
     constexpr bool kOut = kMode != kStates;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int ndvb = (a.Dv + DVB - 1) / DVB;
     const int dv0 = (int)(blockIdx.x % ndvb) * DVB;
     const int h = (int)(blockIdx.x / ndvb % a.H);
@@ -122,9 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], (i == PREADY || i == PREADY + 1) ? 8
-                                    : i == VREADY || i == SREADY || i == EPI ? 4
-                                                                             : 1);
+                mbar_init(&bars[i], i == PREADY || i == PREADY + 1 || i == VREADY || i == SREADY ? 8 : i == EPI ? 4 : 1);
             *stop = 0;
             fence_mbar_init();
         }
@@ -137,12 +203,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const float l = a.log_decay[h];
-    const int ksteps = a.Dk > 64 ? 8 : 4;
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
 
-    if (warp == kWarpTma) {
-        if (lane == 0) {
+    if (warp >= kWarpTma) {
+        regs_fewer<56>();
+        if (warp == kWarpTma && lane == 0) {
             int last0 = -1, last1 = -1;  // last chunk loaded into each stage
             const int boxes = a.Dk > 64 ? 2 : 1;
             for (int c = 0; c < nc; ++c) {
@@ -151,90 +217,104 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 uint8_t* st = sm + s * kStage;
                 const int r = (int)chunk_row(c);
                 mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
+                if (s) last1 = c;
+                else last0 = c;
                 for (int b = 0; b < boxes; ++b) {
                     tma_load_3d(st + OFF_K + b * kBox, &prm.tk, &bars[FULL + s], b * 64, h / a.gk, r);
                     if (kOut) tma_load_3d(st + b * kBox, &prm.tq, &bars[FULL + s], b * 64, h / a.gq, r);
                 }
                 tma_load_3d(st + OFF_V, &prm.tv, &bars[FULL + s], dv0, h / a.gv, r);
-                if (s) last1 = c;
-                else last0 = c;
             }
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
             if (last0 >= 0) mbar_wait(&bars[FULL], (last0 >> 1) & 1, nullptr, 100000000ull);
             if (last1 >= 0) mbar_wait(&bars[FULL + 1], (last1 >> 1) & 1, nullptr, 100000000ull);
         }
-    } else if (warp == kWarpMma) {
-        if (lane == 0) {
+        if (warp == kWarpMma) {
+            // The whole warp runs this loop, so that descriptors stay in uniform registers; one elected lane issues.
             constexpr uint32_t ID_P = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t ID_Y = idesc_bf16_f32(128, 64, false, true);
             constexpr uint32_t ID_DS = idesc_bf16_f32(128, 64, true, true);
-            const uint32_t base = smem_u32(sm);
-            const uint64_t dVP = sw128_desc(base + OFF_VP, 16384, 1024), dS = sw128_desc(base + OFF_S, 16384, 1024);
+            uint32_t base = smem_u32(sm);
             auto scores = [&](int c) {  // P(c) = Q K^T
-                const uint32_t st = base + (c & 1) * kStage;
+                const uint32_t st = base + (c & 1) * kStage, d = tmem + COL_P + (c & 1) * 128;
                 const uint64_t dQ = sw128_desc(st, 16, 1024), dK = sw128_desc(st + OFF_K, 16, 1024);
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                    mma_bf16(tmem + COL_P + (c & 1) * 128, dQ + o, dK + o, ID_P, k > 0);
+                if (elect_one()) {
+                    mma_k64<false>(d, dQ, dK, ID_P, 0);
+                    if (a.Dk > 64) mma_k64<false>(d, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
+                    mma_commit(&bars[PFULL + (c & 1)]);
                 }
-                mma_commit(&bars[PFULL + (c & 1)]);
+                __syncwarp();
             };
             int issued = 0;  // chunks whose scores are under way
             for (int c = 0; c < nc; ++c) {
                 const int s = c & 1;
+                // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
+                // of being kept (and spilled) over the loop
+                asm volatile("" : "+r"(base));
                 const uint32_t st = base + s * kStage;
+                const uint64_t dVP = sw128_desc(base + OFF_VP, 16384, 1024), dS = sw128_desc(base + OFF_S, 16384, 1024);
                 if (kOut && issued <= c) {
-                    if (!mbar_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                    if (!warp_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
                     tc_fence_after();
                     scores(c);
                     issued = c + 1;
                 }
                 // dS(c) = K^T V' (V' is written after the tiles have landed)
-                if (!mbar_wait(&bars[VREADY], c & 1, stop)) { *stop = 1; break; }
+                if (!warp_wait(&bars[VREADY], c & 1, stop)) { *stop = 1; break; }
                 tc_fence_after();
                 const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16(tmem + COL_DS + s * 64, dKt + k * 128, dVP + ((t * kBox) >> 4) + k * 128, ID_DS,
-                                 t > 0 || k > 0);
-                mma_commit(&bars[DSFULL]);
+                    for (int k = 0; k < 8 * kTerms; ++k)  // V' parts lie behind one another: 8 steps are a box
+                        mma_bf16(tmem + COL_DS + s * 64, dKt + (k & 7) * 128, dVP + k * 128, ID_DS, k > 0);
+                    mma_commit(&bars[DSFULL]);
+                }
+                __syncwarp();
                 if (kOut) {
                     // Y2(c) = Q S, once S is written and the chunk before has been read out
-                    if (!mbar_wait(&bars[SREADY], c & 1, stop) || (c >= 1 && !mbar_wait(&bars[EPI], (c - 1) & 1, stop))) {
+                    if (!warp_wait(&bars[SREADY], c & 1, stop) ||
+                        (c >= 1 && !warp_wait(&bars[EPI], (c - 1) & 1, stop))) {
                         *stop = 1;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t dQ = sw128_desc(st, 16, 1024);
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + COL_Y2, dQ + (((k >> 2) * kBox + (k & 3) * 32) >> 4), dS + k * 128, ID_Y, k > 0);
-                    mma_commit(&bars[Y2DONE]);
+                    if (elect_one()) {
+                        mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 0);
+                        if (a.Dk > 64) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
+                        mma_commit(&bars[Y2DONE]);
+                    }
+                    __syncwarp();
                     // the next chunk's scores, if its tiles are here already (never waited for: this chunk's
                     // stage has to be freed for the load behind it)
-                    if (c + 1 < nc && mbar_try_wait(&bars[FULL + (s ^ 1)], ((c + 1) >> 1) & 1)) {
+                    if (c + 1 < nc && __all_sync(0xffffffffu, mbar_test(&bars[FULL + (s ^ 1)], ((c + 1) >> 1) & 1))) {
                         tc_fence_after();
                         scores(c + 1);
                         issued = c + 2;
                     }
                     // Y1(c) = P V
-                    if (!mbar_wait(&bars[PREADY + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                    if (!warp_wait(&bars[PREADY + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
                     tc_fence_after();
                     const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
+                    const uint32_t p = tmem + COL_P + s * 128;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
-                        mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + s * 128 + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128,
-                                    ID_Y, k > 0);
-                    mma_commit(&bars[YFULL]);
+                        for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
+                            mma_bf16_ts(tmem + COL_Y1, p + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y, k > 0);
+                        mma_commit(&bars[YFULL]);
+                    }
+                    __syncwarp();
                 }
-                mma_commit(&bars[EMPTY + s]);
+                if (elect_one()) mma_commit(&bars[EMPTY + s]);
+                __syncwarp();
             }
             // nothing may still be running on the tensor cores when TMEM is released
-            mma_commit(&bars[MMADONE]);
+            if (elect_one()) mma_commit(&bars[MMADONE]);
+            __syncwarp();
             mbar_wait(&bars[MMADONE], 0, nullptr, 100000000ull);
         }
     } else if (warp < 8) {
+        regs_more<104>();
         if (kOut) {
             // ---- scores: row `row`, columns 64 half .. 64 half + 63 ----
             const int j0 = (warp >> 2) * 64;
@@ -268,24 +348,27 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 warp_arrive(&bars[PREADY + s], lane);
             }
         }
-    } else if (warp < 12) {
-        // ---- V' and S: tile row / key row `row` ----
-        float S[DVB];
+    } else if (warp < kWarpOut) {
+        // ---- V' and S: tile row / key row `row`, 32 of the 64 channels ----
+        regs_fewer<72>();
+        const int half = (warp >> 2) & 1, d0 = dv0 + half * kHalf;
+        const int nh = min(kHalf, a.Dv - d0);
+        float S[kHalf];
         const size_t size = (size_t)a.Dk * a.Dv;
         const float* init = kMode == kOutputs ? a.seg_state + ((size_t)slot * a.H + h) * size
                             : kMode == kStates || !a.init ? nullptr
                                                           : a.init + ((size_t)g.seq * a.H + h) * size;
         const bool init_t = kMode == kWhole && a.init_t;
 #pragma unroll
-        for (int d = 0; d < DVB; ++d)
-            S[d] = init && row < a.Dk && d < nv
-                       ? init[init_t ? (size_t)(dv0 + d) * a.Dk + row : (size_t)row * a.Dv + dv0 + d]
+        for (int d = 0; d < kHalf; ++d)
+            S[d] = init && row < a.Dk && d < nh
+                       ? init[init_t ? (size_t)(d0 + d) * a.Dk + row : (size_t)row * a.Dv + d0 + d]
                        : 0.f;
         auto publish = [&] {  // the bf16 copy that Y2 reads
             uint8_t* p = sm + OFF_S;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(p + sw128_off(row, i)) =
+            for (int i = 0; i < kHalf / 8; ++i)
+                *reinterpret_cast<uint4*>(p + sw128_off(row, half * 4 + i)) =
                     make_uint4(pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
                                pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
             fence_async_smem();
@@ -304,14 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t o = sw128_off(row, i);
                     const uint4 z = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(st + OFF_K + o) = z;
-                    *reinterpret_cast<uint4*>(st + OFF_K + kBox + o) = z;
-                    *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
+                    *reinterpret_cast<uint4*>(st + OFF_K + half * kBox + o) = z;
+                    if (i / 4 == half) *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t o = sw128_off(row, i);
+            for (int i = 0; i < kHalf / 8; ++i) {
+                const uint32_t o = sw128_off(row, half * 4 + i);
                 const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                 uint32_t part[kTerms][4];
@@ -351,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const int n = chunk_n(c);
             const float e = n == C ? decay_full : decay_pow(l, n);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < kHalf / 16; ++b) {
                 float v[16];
-                tmem_ld16(lane_base + COL_DS + (c & 1) * 64 + b * 16, v);
+                tmem_ld16(lane_base + COL_DS + (c & 1) * 64 + half * kHalf + b * 16, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[b * 16 + j] = fmaf(e, S[b * 16 + j], v[j]);
@@ -370,49 +452,39 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                      : kMode == kWhole ? (a.final_state ? a.final_state + ((size_t)g.seq * a.H + h) * size : nullptr)
                                        : nullptr;
         if (ok && fin && row < a.Dk) {
-            float* p = fin + (size_t)row * a.Dv + dv0;
+            float* p = fin + (size_t)row * a.Dv + d0;
 #pragma unroll
-            for (int d = 0; d < DVB; d += 4)
-                if (d < nv) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
+            for (int d = 0; d < kHalf; d += 4)
+                if (d < nh) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
         }
-    } else if (warp < 16) {
+    } else {
+        regs_fewer<72>();
         if (kOut) {
             // ---- outputs: tile row `row` ----
             auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
             const float e_full = coefficient(C);
+            // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
+            const bool wide = a.Dv * sizeof(TO) % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
             for (int c = 0; c < nc; ++c) {
                 const int n = chunk_n(c);
                 const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
                 if (!warp_wait(&bars[YFULL], c & 1, stop)) { *stop = 1; break; }
                 tc_fence_after();
-                float o[DVB];
+                TO* dst = static_cast<TO*>(a.o) + (chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0;
+                const int live = row < n ? nv : 0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     float x[16], y[16];
                     tmem_ld16(lane_base + COL_Y1 + b * 16, x);
                     tmem_ld16(lane_base + COL_Y2 + b * 16, y);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[b * 16 + j] = fmaf(e, y[j], x[j]);
-                }
-                tc_fence_before();
-                warp_arrive(&bars[EPI], lane);
-                if (row < n) {
-                    TO* dst = static_cast<TO*>(a.o) + (chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0;
-#pragma unroll
-                    for (int d = 0; d < DVB; d += 8) {
-                        if (d < nv) {
-                            if constexpr (sizeof(TO) == 2) {
-                                *reinterpret_cast<uint4*>(dst + d) =
-                                    make_uint4(pack_bf2(o[d], o[d + 1]), pack_bf2(o[d + 2], o[d + 3]),
-                                               pack_bf2(o[d + 4], o[d + 5]), pack_bf2(o[d + 6], o[d + 7]));
-                            } else {
-                                *reinterpret_cast<float4*>(dst + d) = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
-                                *reinterpret_cast<float4*>(dst + d + 4) =
-                                    make_float4(o[d + 4], o[d + 5], o[d + 6], o[d + 7]);
-                            }
-                        }
+                    if (b == 3) {
+                        tc_fence_before();
+                        warp_arrive(&bars[EPI], lane);
                     }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = fmaf(e, y[j], x[j]);
+                    store16(dst + b * 16, x, live - b * 16, wide);
                 }
             }
         }
@@ -440,8 +512,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Rows of one role: [rows][heads][width] with rows `stride` elements apart; boxes of 128 rows x 64 channels of a
-// head, 128-byte swizzle, zeros outside.
+// Rows of one role: [rows][heads][width] with rows `stride` elements apart; boxes of 128 rows x 128 bytes of a head,
+// 128-byte swizzle, zeros outside.
 bool make_map(CUtensorMap* m, const void* base, int width, int heads, int64_t rows, int64_t stride) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;

@@ -579,22 +579,51 @@ def mimo_decode_step(x, dt, B, C, z, A, D, dt_bias, ssm_state, y=None, y_dtype=N
     return y
 
 
-def _act_code(t, name="q") -> int:
-    if t.dtype == torch.bfloat16:
-        return SSD_BF16
-    if t.dtype == torch.float32:
-        return SSD_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+_ACT_CODES = {torch.bfloat16: SSD_BF16, torch.float32: SSD_F32}
+
+
+def _act_code(t) -> int:
+    code = _ACT_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"activations must be bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+# The operators below are also called for single tokens, where the binding's own time is most of a call: checks
+# take the short way for a tensor that is as expected (a few attribute reads) and the full one only to say
+# what is wrong, and pointers go to ctypes as integers.
+
+def _arg(t, name, shape, dtype, device) -> int:
+    """The address of a contiguous tensor of the expected shape, type and device."""
+    if t is None or t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _rows_arg(t, name, shape, dtype, device, width, packed) -> tuple:
+    """The address of per-token rows and the elements between consecutive tokens (see _row_stride); ``packed``:
+    one leading dimension of tokens, else batch and tokens."""
+    if t is not None and t.shape == shape and t.dtype is dtype and t.device == device:
+        if t.is_contiguous():
+            return t.data_ptr(), width
+        if packed:
+            rs, h, d = t.stride()
+            if d == 1 and h == shape[2] and shape[0] > 1:
+                return t.data_ptr(), rs
+    if packed and t is not None:
+        return t.data_ptr(), _row_stride(t.unsqueeze(0), name, (1,) + tuple(shape), dtype, device)
+    return t.data_ptr() if t is not None else 0, _row_stride(t, name, shape, dtype, device)
 
 
 def _enqueue(what, dev, *args):
     """Calls ``what`` with the current stream of ``dev`` (which need not be the current device)."""
-    fn = getattr(lib(), what)
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, _stream_ptr(dev))
+    fn = getattr(_lib or lib(), what)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream_ptr(dev))
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise SsdError(st, what)
 
@@ -605,10 +634,11 @@ def _workspace(workspace, need, dev):
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         if workspace.numel() * workspace.element_size() >= need:
-            return workspace, workspace.numel() * workspace.element_size()
+            return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if not need:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=dev), need
+        return None, None, 0
+    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), need
 
 
 def _cuda_device(t, name):
@@ -618,20 +648,20 @@ def _cuda_device(t, name):
 
 
 def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved):
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    """Checked inputs of the norm and rotation: device, dims, strides, dtype code, addresses."""
+    dev, sq, sk, dtype = _cuda_device(q, "q"), q.shape, k.shape, q.dtype
+    if len(sq) not in (3, 4) or len(sk) != len(sq):
         raise ValueError("q and k must be [T, heads, D] or [Bt, L, heads, D]")
-    dev = _cuda_device(q, "q")
-    lead, Hq, Hk, D = tuple(q.shape[:-2]), q.shape[-2], k.shape[-2], q.shape[-1]
-    rows = lead if len(lead) == 2 else (1,) + lead
-    rs = SsdQkStrides(*[_row_stride(t if len(lead) == 2 else t.unsqueeze(0), name, rows + (n, D), q.dtype, dev)
-                        for name, t, n in (("q", q, Hq), ("k", k, Hk))])
-    _check(q_weight, "q_weight", (D,), torch.float32, dev)
-    _check(k_weight, "k_weight", (D,), torch.float32, dev)
-    _check(positions, "positions", lead, torch.int64, dev)
+    lead, Hq, Hk, D = sq[:-2], sq[-2], sk[-2], sq[-1]
+    packed = len(lead) == 1
+    pq, rq = _rows_arg(q, "q", sq, dtype, dev, Hq * D, packed)
+    pk, rk = _rows_arg(k, "k", lead + (Hk, D), dtype, dev, Hk * D, packed)
     half = inv_freq.numel()
-    _check(inv_freq, "inv_freq", (half,), torch.float32, dev)
-    dims = SsdQkDims(rows[0] * rows[1], Hq, Hk, D, 2 * half, int(bool(interleaved)))
-    return dev, dims, rs, _act_code(q)
+    ptrs = (pq, pk, _arg(q_weight, "q_weight", (D,), torch.float32, dev),
+            _arg(k_weight, "k_weight", (D,), torch.float32, dev), _arg(positions, "positions", lead, torch.int64, dev),
+            _arg(inv_freq, "inv_freq", (half,), torch.float32, dev))
+    dims = SsdQkDims(lead[0] if packed else lead[0] * lead[1], Hq, Hk, D, 2 * half, 1 if interleaved else 0)
+    return dev, dims, SsdQkStrides(rq, rk), _act_code(q), ptrs
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interleaved=False, q_out=None, k_out=None):
@@ -643,15 +673,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, interl
     positions * inv_freq (taken in fp64), in pairs (p, p + rot/2), or (2p, 2p + 1) with ``interleaved``.
     Returns (q_out, k_out), contiguous; a contiguous input may be its own output.
     """
-    dev, dims, rs, code = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
+    dev, dims, rs, code, ptrs = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    _check(q_out, "q_out", tuple(q.shape), q.dtype, dev)
-    _check(k_out, "k_out", tuple(k.shape), q.dtype, dev)
-    _enqueue("ssd_qk_norm_rope", dev, ctypes.byref(dims), code, float(eps), ctypes.byref(rs), _ptr(q), _ptr(k),
-             _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), _ptr(q_out), _ptr(k_out))
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    _enqueue("ssd_qk_norm_rope", dev, ctypes.byref(dims), code, eps, ctypes.byref(rs), *ptrs,
+             _arg(q_out, "q_out", q.shape, q.dtype, dev), _arg(k_out, "k_out", k.shape, q.dtype, dev))
     return q_out, k_out
 
 
@@ -659,16 +687,14 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, i
                           workspace=None):
     """Gradients of ``qk_norm_rope`` from those of its outputs (contiguous).  Returns a dict keyed by the input
     they belong to: q, k (the activation dtype, contiguous), q_weight, k_weight (fp32)."""
-    dev, dims, rs, code = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
-    _check(dq_out, "dq_out", tuple(q.shape), q.dtype, dev)
-    _check(dk_out, "dk_out", tuple(k.shape), q.dtype, dev)
+    dev, dims, rs, code, ptrs = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, interleaved)
+    dy = (_arg(dq_out, "dq_out", q.shape, q.dtype, dev), _arg(dk_out, "dk_out", k.shape, q.dtype, dev))
     out = {"q": torch.empty(q.shape, dtype=q.dtype, device=dev), "k": torch.empty(k.shape, dtype=q.dtype, device=dev),
            "q_weight": torch.empty_like(q_weight), "k_weight": torch.empty_like(k_weight)}
-    workspace, ws_bytes = _workspace(workspace, int(lib().ssd_qk_norm_rope_backward_workspace_bytes(
-        ctypes.byref(dims))), dev)
-    _enqueue("ssd_qk_norm_rope_backward", dev, ctypes.byref(dims), code, float(eps), ctypes.byref(rs), _ptr(dq_out),
-             _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
-             _ptr(out["q"]), _ptr(out["k"]), _ptr(out["q_weight"]), _ptr(out["k_weight"]), _ptr(workspace), ws_bytes)
+    workspace, ws, ws_bytes = _workspace(workspace, lib().ssd_qk_norm_rope_backward_workspace_bytes(
+        ctypes.byref(dims)), dev)
+    _enqueue("ssd_qk_norm_rope_backward", dev, ctypes.byref(dims), code, eps, ctypes.byref(rs), *dy, *ptrs,
+             *[t.data_ptr() for t in out.values()], ws, ws_bytes)
     return out
 
 
@@ -683,35 +709,39 @@ def _offsets(cu_seqlens, dev):
     return cu_seqlens, cu_seqlens.numel() - 1
 
 
-def _linear_attn_prefill(q, k, v, log_decay, cu_seqlens, init_state, scale, workspace, o, final_state):
-    dev = _cuda_device(q, "q")
-    packed = cu_seqlens is not None
+def _linear_attn_dims(q, k, v, cu_seqlens):
+    """Device, offsets, leading shape, sizes and state shape of a linear-attention call."""
+    dev, packed = _cuda_device(q, "q"), cu_seqlens is not None
+    sq = q.shape
+    if len(sq) != (3 if packed else 4) or k.dim() != len(sq) or v.dim() != len(sq):
+        raise ValueError("q, k, v must be [T, heads, D] with cu_seqlens, else [Bt, L, heads, D]")
+    lead, H, Dk, Hk, Dv = sq[:-2], sq[-2], sq[-1], k.shape[-2], v.shape[-1]
+    Bt = lead[0]
     if packed:
         cu_seqlens, Bt = _offsets(cu_seqlens, dev)
-        rows = (1, q.shape[0])
-    else:
-        Bt = q.shape[0]
-        rows = tuple(q.shape[:2])
-    H, Dk, Hk, Dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
-    rs = SsdLinearAttnStrides(*[_row_stride(t.unsqueeze(0) if packed else t, name, rows + tail, q.dtype, dev)
-                                for name, t, tail in (("q", q, (H, Dk)), ("k", k, (Hk, Dk)), ("v", v, (Hk, Dv)))])
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    state = (Bt, H, Dk, Dv)
-    if init_state is not None:
-        _check(init_state, "init_state", state, torch.float32, dev)
+    return (dev, cu_seqlens, lead, H, Hk, Dk, Dv, SsdLinearAttnDims(Bt, lead[-1], H, Hk, Dk, Dv), (Bt, H, Dk, Dv),
+            cu_seqlens.data_ptr() if packed else None)
+
+
+def _linear_attn_prefill(q, k, v, log_decay, cu_seqlens, init_state, scale, workspace, o, final_state):
+    dev, cu_seqlens, lead, H, Hk, Dk, Dv, dims, state, cu = _linear_attn_dims(q, k, v, cu_seqlens)
+    packed, dtype = cu is not None, q.dtype
+    code = _act_code(q)
+    pq, rq = _rows_arg(q, "q", q.shape, dtype, dev, H * Dk, packed)
+    pk, rk = _rows_arg(k, "k", lead + (Hk, Dk), dtype, dev, Hk * Dk, packed)
+    pv, rv = _rows_arg(v, "v", lead + (Hk, Dv), dtype, dev, Hk * Dv, packed)
+    ld = _arg(log_decay, "log_decay", (H,), torch.float32, dev)
+    init = None if init_state is None else _arg(init_state, "init_state", state, torch.float32, dev)
     if o is None:
-        o = torch.empty(tuple(q.shape[:-1]) + (Dv,), dtype=q.dtype, device=dev)
+        o = torch.empty(lead + (H, Dv), dtype=dtype, device=dev)
     if final_state is None:
         final_state = torch.empty(state, dtype=torch.float32, device=dev)
-    _check(o, "o", tuple(q.shape[:-1]) + (Dv,), q.dtype, dev)
-    _check(final_state, "final_state", state, torch.float32, dev)
-    dims = SsdLinearAttnDims(Bt, rows[1], H, Hk, Dk, Dv)
-    code = _act_code(q)
-    need = int(lib().ssd_linear_attn_prefill_workspace_bytes(ctypes.byref(dims), code, int(packed)))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    _enqueue("ssd_linear_attn_prefill", dev, ctypes.byref(dims), code, _ptr(log_decay),
-             float(Dk ** -0.5 if scale is None else scale), ctypes.byref(rs), _ptr(cu_seqlens), _ptr(q), _ptr(k),
-             _ptr(v), _ptr(init_state), _ptr(o), _ptr(final_state), _ptr(workspace), ws_bytes)
+    po = _arg(o, "o", lead + (H, Dv), dtype, dev)
+    fin = _arg(final_state, "final_state", state, torch.float32, dev)
+    workspace, ws, ws_bytes = _workspace(workspace, lib().ssd_linear_attn_prefill_workspace_bytes(
+        ctypes.byref(dims), code, packed), dev)
+    _enqueue("ssd_linear_attn_prefill", dev, ctypes.byref(dims), code, ld, Dk ** -0.5 if scale is None else scale,
+             ctypes.byref(SsdLinearAttnStrides(rq, rk, rv)), cu, pq, pk, pv, init, po, fin, ws, ws_bytes)
     return o, final_state
 
 
@@ -723,8 +753,6 @@ def linear_attn_prefill(q, k, v, log_decay, init_state=None, scale=None, workspa
     [Bt, H, Dk, Dv] fp32 or None; scale: Dk ** -0.5 by default.  Dk and Dv are multiples of 8 up to 128.
     Returns (o [Bt, L, H, Dv], final_state [Bt, H, Dk, Dv] fp32); final_state may be init_state's tensor.
     """
-    if q.dim() != 4:
-        raise ValueError("q must be [Bt, L, H, Dk]")
     return _linear_attn_prefill(q, k, v, log_decay, None, init_state, scale, workspace, o, final_state)
 
 
@@ -737,8 +765,8 @@ def linear_attn_prefill_varlen(q, k, v, log_decay, cu_seqlens, init_state=None, 
     Returns (o [T, H, Dv], final_state [nseq, H, Dk, Dv]); rows outside every sequence are not written.
     Offsets that are out of order or out of range are reported by device_status().
     """
-    if q.dim() != 3:
-        raise ValueError("q must be [T, H, Dk]")
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
     return _linear_attn_prefill(q, k, v, log_decay, cu_seqlens, init_state, scale, workspace, o, final_state)
 
 
@@ -747,38 +775,29 @@ def linear_attn_backward(q, k, v, log_decay, do, init_state=None, d_final_state=
     """Gradients of ``linear_attn_prefill`` (or, with ``cu_seqlens``, of ``linear_attn_prefill_varlen``).
 
     Inputs as for the forward (contiguous); do is shaped as o, d_final_state as final_state, or None.
-    Returns a dict keyed by the input they belong to: q, k, v (the activation dtype) and, with
-    ``want_init_grads``, init_state (fp32): the gradients of sum(do * o) + sum(d_final_state * final_state).
+    Returns a dict keyed by the input they belong to: q, k, v (the activation dtype; rows outside every packed
+    sequence are not written) and, with ``want_init_grads``, init_state (fp32): the gradients of
+    sum(do * o) + sum(d_final_state * final_state).
     """
-    dev = _cuda_device(q, "q")
-    packed = cu_seqlens is not None
-    if q.dim() != (3 if packed else 4):
-        raise ValueError("q must be [T, H, Dk] with cu_seqlens, else [Bt, L, H, Dk]")
-    if packed:
-        cu_seqlens, Bt = _offsets(cu_seqlens, dev)
-    else:
-        Bt = q.shape[0]
-    lead = tuple(q.shape[:-2])
-    H, Dk, Hk, Dv = q.shape[-2], q.shape[-1], k.shape[-2], v.shape[-1]
-    for name, t, tail in (("q", q, (H, Dk)), ("k", k, (Hk, Dk)), ("v", v, (Hk, Dv)), ("do", do, (H, Dv))):
-        _check(t, name, lead + tail, q.dtype, dev)
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    state = (Bt, H, Dk, Dv)
-    if init_state is not None:
-        _check(init_state, "init_state", state, torch.float32, dev)
-    if d_final_state is not None:
-        _check(d_final_state, "d_final_state", state, torch.float32, dev)
+    dev, cu_seqlens, lead, H, Hk, Dk, Dv, dims, state, cu = _linear_attn_dims(q, k, v, cu_seqlens)
+    code, dtype = _act_code(q), q.dtype
+    pq = _arg(q, "q", lead + (H, Dk), dtype, dev)
+    pk = _arg(k, "k", lead + (Hk, Dk), dtype, dev)
+    pv = _arg(v, "v", lead + (Hk, Dv), dtype, dev)
+    pdo = _arg(do, "do", lead + (H, Dv), dtype, dev)
+    ld = _arg(log_decay, "log_decay", (H,), torch.float32, dev)
+    init = None if init_state is None else _arg(init_state, "init_state", state, torch.float32, dev)
+    dfin = None if d_final_state is None else _arg(d_final_state, "d_final_state", state, torch.float32, dev)
     out = {"q": torch.empty_like(q), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+    dinit = None
     if want_init_grads:
         out["init_state"] = torch.empty(state, dtype=torch.float32, device=dev)
-    dims = SsdLinearAttnDims(Bt, lead[-1], H, Hk, Dk, Dv)
-    code = _act_code(q)
-    need = int(lib().ssd_linear_attn_backward_workspace_bytes(ctypes.byref(dims), code, int(packed)))
-    workspace, ws_bytes = _workspace(workspace, need, dev)
-    _enqueue("ssd_linear_attn_backward", dev, ctypes.byref(dims), code, _ptr(log_decay),
-             float(Dk ** -0.5 if scale is None else scale), _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
-             _ptr(init_state), _ptr(do), _ptr(d_final_state), _ptr(out["q"]), _ptr(out["k"]), _ptr(out["v"]),
-             _ptr(out.get("init_state")), _ptr(workspace), ws_bytes)
+        dinit = out["init_state"].data_ptr()
+    workspace, ws, ws_bytes = _workspace(workspace, lib().ssd_linear_attn_backward_workspace_bytes(
+        ctypes.byref(dims), code, cu is not None), dev)
+    _enqueue("ssd_linear_attn_backward", dev, ctypes.byref(dims), code, ld, Dk ** -0.5 if scale is None else scale, cu,
+             pq, pk, pv, init, pdo, dfin, out["q"].data_ptr(), out["k"].data_ptr(), out["v"].data_ptr(), dinit, ws,
+             ws_bytes)
     return out
 
 
@@ -788,19 +807,17 @@ def linear_attn_decode_step(q, k, v, log_decay, state, scale=None, o=None):
     q [Bt, H, Dk], k [Bt, Hk, Dk], v [Bt, Hk, Dv] (bf16 or fp32); log_decay [H] fp32; state [Bt, H, Dk, Dv] fp32.
     Returns o [Bt, H, Dv].
     """
-    dev = _cuda_device(q, "q")
+    dev, dtype = _cuda_device(q, "q"), q.dtype
     Bt, H, Dk = q.shape
     Hk, Dv = k.shape[1], v.shape[2]
-    for name, t, shp in (("q", q, (Bt, H, Dk)), ("k", k, (Bt, Hk, Dk)), ("v", v, (Bt, Hk, Dv))):
-        _check(t, name, shp, q.dtype, dev)
-    _check(log_decay, "log_decay", (H,), torch.float32, dev)
-    _check(state, "state", (Bt, H, Dk, Dv), torch.float32, dev)
     if o is None:
-        o = torch.empty((Bt, H, Dv), dtype=q.dtype, device=dev)
-    _check(o, "o", (Bt, H, Dv), q.dtype, dev)
+        o = torch.empty((Bt, H, Dv), dtype=dtype, device=dev)
     dims = SsdLinearAttnDims(Bt, 1, H, Hk, Dk, Dv)
-    _enqueue("ssd_linear_attn_decode_step", dev, ctypes.byref(dims), _act_code(q), _ptr(log_decay),
-             float(Dk ** -0.5 if scale is None else scale), _ptr(q), _ptr(k), _ptr(v), _ptr(state), _ptr(o))
+    _enqueue("ssd_linear_attn_decode_step", dev, ctypes.byref(dims), _act_code(q),
+             _arg(log_decay, "log_decay", (H,), torch.float32, dev), Dk ** -0.5 if scale is None else scale,
+             _arg(q, "q", (Bt, H, Dk), dtype, dev), _arg(k, "k", (Bt, Hk, Dk), dtype, dev),
+             _arg(v, "v", (Bt, Hk, Dv), dtype, dev), _arg(state, "state", (Bt, H, Dk, Dv), torch.float32, dev),
+             _arg(o, "o", (Bt, H, Dv), dtype, dev))
     return o
 
 

@@ -94,9 +94,8 @@ def test_prefill_refuses(L):
         assert prefill_call(L, la_dims(), scale=scale) == SHAPE
     for name in ("log_decay", "q", "k", "v", "o", "final"):
         assert prefill_call(L, la_dims(), ptrs={name: None}) == NULL, name
-    for i, name in ((1, "q"), (2, "k"), (3, "v"), (4, "init"), (6, "final")):
+    for i, name in ((1, "q"), (2, "k"), (3, "v"), (4, "init"), (5, "o"), (6, "final")):
         assert prefill_call(L, la_dims(), ptrs={name: vp(i, 8)}) == ALIGN, name
-    assert prefill_call(L, la_dims(), ptrs=dict(o=vp(5, 16))) == ALIGN
     assert prefill_call(L, la_dims(), ptrs=dict(log_decay=vp(0, 2))) == ALIGN
     assert prefill_call(L, la_dims(), ptrs=dict(cu=vp(7, 4))) == ALIGN
     w = (8 * 64, 4 * 64, 4 * 128)
@@ -155,7 +154,7 @@ def test_backward_refuses(L):
     for name in ("log_decay", "q", "k", "v", "do", "dq", "dk", "dv"):
         assert backward_call(L, la_dims(), ptrs={name: None}) == NULL, name
     for i, name in enumerate(names):
-        off = 2 if name == "log_decay" else 16 if name in ("dq", "dk", "dv") else 8
+        off = 2 if name == "log_decay" else 8
         assert backward_call(L, la_dims(), ptrs={name: vp(i, off)}) == ALIGN, name
     for out in ("dq", "dk", "dv", "d_init"):
         for i, name in enumerate(names):
