@@ -409,8 +409,8 @@ SSD_API ssd_status ssd_set_timing_events(void* before_main, void* after_main);
  * Packed batches: cu_seqlens is a device array of batch + 1 non-decreasing row
  * offsets, sequence s = rows cu_seqlens[s] .. cu_seqlens[s+1]-1; rows outside
  * every sequence are neither used nor written.  Offsets out of order or out of
- * range are reported by ssd_device_status (SSD_ERR_SHAPE) and that sequence is
- * taken as empty.
+ * range are reported by ssd_device_status (SSD_ERR_SHAPE); no memory outside the
+ * buffers is touched, and the outputs of that call are unspecified.
  */
 typedef struct {
     int64_t batch;     /* sequences                                             */

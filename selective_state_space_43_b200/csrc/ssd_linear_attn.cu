@@ -84,8 +84,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(DecodeArgs a) {
 
 // ---- joining segments ---------------------------------------------------------------------------------------
 // R <- e^{l n_i} R + (state of segment i alone), in scan order; four state elements per thread.
-__global__ void __launch_bounds__(256) combine_kernel(ScanArgs a) {
-    const int64_t b = blockIdx.x;
+struct CombineArgs {
+    ScanArgs scan[2];
+};
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ CombineArgs both) {
+    const ScanArgs& a = both.scan[blockIdx.x >= both.scan[0].batch];
+    const int64_t b = blockIdx.x % a.batch;
     const int h = blockIdx.y, e = (blockIdx.z * 256 + threadIdx.x) * 4, size = a.Dk * a.Dv;
     const Span s = sequence_span(a, b);
     if (!s.ok && h == 0 && e == 0) atomicOr(a.err, kErrBadSeqlens);
@@ -146,9 +150,10 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_combine(const ScanArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)a.batch, a.H, (a.Dk * a.Dv + 1023) / 1024);
-    combine_kernel<<<grid, 256, 0, st>>>(a);
+cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st) {
+    const ScanArgs& a = scans[0];  // the scans of one call have the same number of states of the same size
+    const dim3 grid((unsigned)(a.batch * count), a.H, (a.Dk * a.Dv + 1023) / 1024);
+    combine_kernel<<<grid, 256, 0, st>>>(CombineArgs{{scans[0], scans[count - 1]}});
     return cudaGetLastError();
 }
 
@@ -216,9 +221,66 @@ template <int NO, int NI> bool outputs_alias(const Buffer (&outs)[NO], const Buf
     return false;
 }
 
-// One scan: whole sequences.
-cudaError_t launch_scan(ScanArgs a, cudaStream_t st) {
-    return a.bf16 ? launch_scan_tc(a, kWhole, st) : launch_scan_simt(a, kWhole, st);
+cudaError_t launch_scans(const ScanArgs* scans, int count, Mode mode, cudaStream_t st) {
+    return scans[0].bf16 ? launch_scan_tc(scans, count, mode, st) : launch_scan_simt(scans, count, mode, st);
+}
+
+// ---- cutting the sequence axis ------------------------------------------------------------------------------
+// A scan walks its rows one chunk behind the other, so a call with few (sequence, head) pairs leaves SMs
+// idle.  Cut into segments it takes two passes (the state each segment leaves, joined, then the outputs from
+// the joined states), which read keys and values twice.  The choice compares modelled times in microseconds:
+// a block costs kStart, and per row kRow for outputs (and states) or kStateRow for states alone; blocks run
+// kSlots at a time; the cut adds two launches (kExtra) and the writing, joining and reading of its states.
+// Measured on B200 with bf16 rows, 8192 rows of 16 heads, 128 x 128: see the figures beside each.
+struct Cost {
+    double start, row, state_row, extra, slots;
+};
+Cost cost_of(bool bf16, int Dk) {
+    // tensor cores, one block per SM: 2.0 us a 128-row chunk, 1.2 us of it for states alone;
+    // CUDA cores, two blocks per SM at Dk = 128
+    return bf16 ? Cost{5.0, 2.0 / 128, 1.2 / 128, 6.0, 148.0}
+                : Cost{5.0, 0.6 * Dk / 128, 0.25 * Dk / 128, 6.0, Dk > 64 ? 296.0 : 592.0};
+}
+// Rows of a segment (a multiple of 128), or 0: whole sequences.  `blocks`: blocks of the output pass for each
+// sequence; `state_blocks`: of the states' pass.
+int64_t segment_rows(int64_t batch, int64_t L, int64_t rows, bool packed, bool bf16, int Dk, int Dv, int64_t H,
+                     int64_t blocks, int64_t state_blocks) {
+    if (batch == 0 || rows == 0) return 0;
+    const Cost k = cost_of(bf16, Dk);
+    const double mean = (double)rows / batch;
+    // the longest of a packed batch is not known here; three times the mean is usual for prompts
+    const double longest = packed ? fmin((double)rows, 3.0 * mean) : (double)L;
+    auto waves = [&](double n) { return n <= k.slots ? 1.0 : packed ? n / k.slots + 0.5 : ceil(n / k.slots); };
+    const double all = (double)batch * blocks;
+    double best = fmax(waves(all) * (k.start + mean * k.row), k.start + longest * k.row);
+    int64_t seg = 0;
+    for (int64_t m = 256; m < longest; m *= 2) {
+        const double slots = packed ? rows / (double)m + 0.5 * batch : batch * ceil((double)L / m);
+        const double bytes = slots * H * Dk * Dv * 4 * 4;  // written, read and written, read
+        const double part = fmin((double)m, mean);
+        const double t = waves(slots * state_blocks) * (k.start + part * k.state_row) +
+                         waves(slots * blocks) * (k.start + part * k.row) + k.extra + bytes / 5e6;
+        if (t < 0.9 * best) {
+            best = t;
+            seg = m;
+        }
+    }
+    return seg;
+}
+int64_t value_blocks(int64_t H, int Dv) { return H * ((Dv + 63) / 64); }
+
+int64_t prefill_segment(const ssd_linear_attn_dims* d, bool bf16, bool packed, int64_t rows) {
+    const int64_t b = value_blocks(d->nheads, d->value_dim);
+    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, b, b);
+}
+int64_t backward_segment(const ssd_linear_attn_dims* d, bool bf16, bool packed, int64_t rows) {
+    const int64_t k = value_blocks(d->nheads, d->key_dim), v = value_blocks(d->nheads, d->value_dim);
+    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, 2 * k + v, k + v);
+}
+// Bytes of one scan's segment states.
+size_t segment_bytes(const ssd_linear_attn_dims* d, bool packed, int64_t rows, int64_t seg) {
+    if (seg == 0) return 0;
+    return (size_t)slot_count(d->batch, d->seqlen, rows, packed, seg) * d->nheads * d->key_dim * d->value_dim * 4;
 }
 
 }  // namespace
@@ -231,9 +293,9 @@ using namespace ssd::la;
 extern "C" {
 
 size_t ssd_linear_attn_prefill_workspace_bytes(const ssd_linear_attn_dims* d, ssd_dtype dtype, int packed) {
-    (void)packed;
-    if (la::check_dims(d, dtype) != SSD_OK) return 0;
-    return 0;
+    int64_t rows;
+    if (la::check_dims(d, dtype) != SSD_OK || count_rows(d, packed != 0, &rows) != SSD_OK) return 0;
+    return segment_bytes(d, packed != 0, rows, prefill_segment(d, dtype == SSD_BF16, packed != 0, rows));
 }
 
 ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* d, ssd_dtype dtype, const float* log_decay, float scale,
@@ -289,19 +351,28 @@ ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* d, ssd_dtype dtyp
     a.batch = d->batch; a.L = d->seqlen; a.rows = rows;
     a.cu = cu_seqlens;
     if (!(a.err = device_error_flag())) return SSD_ERR_CUDA;
-    return launch_scan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    a.seg_len = prefill_segment(d, a.bf16, packed, rows);
+    if (a.seg_len == 0) return launch_scans(&a, 1, kWhole, cs) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    a.slots = slot_count(a.batch, a.L, rows, packed, a.seg_len);
+    a.seg_state = static_cast<float*>(workspace);
+    cudaError_t e = launch_scans(&a, 1, kStates, cs);
+    if (e == cudaSuccess) e = launch_combine(&a, 1, cs);
+    if (e == cudaSuccess) e = launch_scans(&a, 1, kOutputs, cs);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 // Bytes of the fp32 per-head gradients of shared keys and values (none when every head has its own).
 static size_t group_bytes(const ssd_linear_attn_dims* d, int64_t rows) {
     if (d->nheads == d->kv_heads) return 0;
-    return (size_t)rows * d->nheads * (d->key_dim > d->value_dim ? d->key_dim : d->value_dim) * 4;
+    return (size_t)rows * d->nheads * (d->key_dim + d->value_dim) * 4;
 }
 
 size_t ssd_linear_attn_backward_workspace_bytes(const ssd_linear_attn_dims* d, ssd_dtype dtype, int packed) {
     int64_t rows;
     if (la::check_dims(d, dtype) != SSD_OK || count_rows(d, packed != 0, &rows) != SSD_OK) return 0;
-    return group_bytes(d, rows);
+    return group_bytes(d, rows) +
+           2 * segment_bytes(d, packed != 0, rows, backward_segment(d, dtype == SSD_BF16, packed != 0, rows));
 }
 
 ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dtype, const float* log_decay, float scale,
@@ -346,46 +417,62 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dty
     base.batch = d->batch; base.L = d->seqlen; base.rows = rows;
     base.cu = cu_seqlens;
     if (!(base.err = device_error_flag())) return SSD_ERR_CUDA;
-    float* shared = group > 1 ? static_cast<float*>(workspace) : nullptr;
+    // workspace: the shared heads' dk and dv, then the segment states of the dq scan and of the dv scan
+    float* ws = static_cast<float*>(workspace);
+    float* dk_heads = group > 1 ? ws : nullptr;
+    float* dv_heads = group > 1 ? ws + (size_t)rows * H * Dk : nullptr;
+    base.seg_len = backward_segment(d, base.bf16, packed, rows);
+    if (base.seg_len) base.slots = slot_count(base.batch, base.L, rows, packed, base.seg_len);
+    float* states = ws + group_bytes(d, rows) / 4;
 
-    ScanArgs a = base;  // dq
-    a.q = d_o; a.rs_q = H * Dv; a.gq = 1;
-    a.k = v; a.rs_k = Hk * Dv; a.gk = group;
-    a.v = k; a.rs_v = Hk * Dk; a.gv = group;
-    a.Dk = (int)Dv; a.Dv = (int)Dk;
-    a.inter_scale = scale; a.w_scale = 1.f;
-    a.init = init_state; a.init_t = true;
-    a.o = dq;
-    cudaError_t e = launch_scan(a, cs);
-    if (e != cudaSuccess) return SSD_ERR_CUDA;
+    ScanArgs a[3];
+    ScanArgs& sq = a[0] = base;  // dq
+    sq.q = d_o; sq.rs_q = H * Dv; sq.gq = 1;
+    sq.k = v; sq.rs_k = Hk * Dv; sq.gk = group;
+    sq.v = k; sq.rs_v = Hk * Dk; sq.gv = group;
+    sq.Dk = (int)Dv; sq.Dv = (int)Dk;
+    sq.inter_scale = scale; sq.w_scale = 1.f;
+    sq.init = init_state; sq.init_t = true;
+    sq.o = dq;
+    sq.o_f32 = dtype == SSD_F32;
+    sq.seg_state = states;
 
-    a = base;  // dk
-    a.reverse = true;
-    a.inter_scale = 1.f; a.w_scale = scale;
-    a.q = v; a.rs_q = Hk * Dv; a.gq = group;
-    a.k = d_o; a.rs_k = H * Dv; a.gk = 1;
-    a.v = q; a.rs_v = H * Dk; a.gv = 1;
-    a.Dk = (int)Dv; a.Dv = (int)Dk;
-    a.init = d_final_state; a.init_t = true;
-    a.o = shared ? shared : dk;
-    a.o_f32 = shared || dtype == SSD_F32;
-    e = launch_scan(a, cs);
-    if (e == cudaSuccess && shared) e = launch_group_sum(shared, dk, rows, (int)Hk, group, (int)Dk, base.bf16, cs);
-    if (e != cudaSuccess) return SSD_ERR_CUDA;
+    ScanArgs& sv = a[1] = base;  // dv, and the initial state's gradient
+    sv.reverse = true;
+    sv.inter_scale = 1.f; sv.w_scale = scale;
+    sv.q = k; sv.rs_q = Hk * Dk; sv.gq = group;
+    sv.k = q; sv.rs_k = H * Dk; sv.gk = 1;
+    sv.v = d_o; sv.rs_v = H * Dv; sv.gv = 1;
+    sv.Dk = (int)Dk; sv.Dv = (int)Dv;
+    sv.init = d_final_state;
+    sv.final_state = d_init_state;
+    sv.o = group > 1 ? dv_heads : dv;
+    sv.o_f32 = group > 1 || dtype == SSD_F32;
+    sv.seg_state = base.seg_len ? states + segment_bytes(d, packed, rows, base.seg_len) / 4 : nullptr;
 
-    a = base;  // dv, and the initial state's gradient
-    a.reverse = true;
-    a.inter_scale = 1.f; a.w_scale = scale;
-    a.q = k; a.rs_q = Hk * Dk; a.gq = group;
-    a.k = q; a.rs_k = H * Dk; a.gk = 1;
-    a.v = d_o; a.rs_v = H * Dv; a.gv = 1;
-    a.Dk = (int)Dk; a.Dv = (int)Dv;
-    a.init = d_final_state;
-    a.final_state = d_init_state;
-    a.o = shared ? shared : dv;
-    a.o_f32 = shared || dtype == SSD_F32;
-    e = launch_scan(a, cs);
-    if (e == cudaSuccess && shared) e = launch_group_sum(shared, dv, rows, (int)Hk, group, (int)Dv, base.bf16, cs);
+    ScanArgs& sk = a[2] = base;  // dk: the dv scan's states, transposed
+    sk.reverse = true;
+    sk.inter_scale = 1.f; sk.w_scale = scale;
+    sk.q = v; sk.rs_q = Hk * Dv; sk.gq = group;
+    sk.k = d_o; sk.rs_k = H * Dv; sk.gk = 1;
+    sk.v = q; sk.rs_v = H * Dk; sk.gv = 1;
+    sk.Dk = (int)Dv; sk.Dv = (int)Dk;
+    sk.init = d_final_state; sk.init_t = true;
+    sk.o = group > 1 ? dk_heads : dk;
+    sk.o_f32 = group > 1 || dtype == SSD_F32;
+    sk.seg_state = sv.seg_state;
+    sk.seg_t = true;
+
+    cudaError_t e;
+    if (base.seg_len) {
+        e = launch_scans(a, 2, kStates, cs);
+        if (e == cudaSuccess) e = launch_combine(a, 2, cs);
+        if (e == cudaSuccess) e = launch_scans(a, 3, kOutputs, cs);
+    } else {
+        e = launch_scans(a, 3, kWhole, cs);
+    }
+    if (e == cudaSuccess && group > 1) e = launch_group_sum(dk_heads, dk, rows, (int)Hk, group, (int)Dk, base.bf16, cs);
+    if (e == cudaSuccess && group > 1) e = launch_group_sum(dv_heads, dv, rows, (int)Hk, group, (int)Dv, base.bf16, cs);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

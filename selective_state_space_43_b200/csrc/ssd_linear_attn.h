@@ -37,7 +37,8 @@ struct ScanArgs {
     int* err;                    // device error word
     // The sequence axis cut into segments of seg_len rows (0: whole sequences), see Segment.
     int64_t seg_len, slots;
-    float* seg_state;            // [slots][H][Dk][Dv]
+    float* seg_state;            // [slots][H][Dk][Dv] ([Dv][Dk] when seg_t: another scan's, joined there)
+    bool seg_t;
 };
 
 // What a launch of a scan kernel does with its rows.
@@ -98,14 +99,15 @@ __device__ inline Segment segment_of(const ScanArgs& a, int64_t slot) {
 // e^{l n} of a head; -inf (a head that keeps nothing) gives e^{l 0} = 1 like every other decay.
 __device__ __forceinline__ float decay_pow(float l, int64_t n) { return n == 0 ? 1.f : expf(l * (float)n); }
 
-// CUDA-core scan.
-cudaError_t launch_scan_simt(const ScanArgs& a, Mode mode, cudaStream_t st);
-// Tensor-core scan (bf16 rows).
-cudaError_t launch_scan_tc(const ScanArgs& a, Mode mode, cudaStream_t st);
+// CUDA-core scan (fp32 rows).
+cudaError_t launch_scan_simt(const ScanArgs* scans, int count, Mode mode, cudaStream_t st);
+// Tensor-core scan (bf16 rows), up to three in one launch.
+cudaError_t launch_scan_tc(const ScanArgs* scans, int count, Mode mode, cudaStream_t st);
 
 // Runs the segments' states into one another: seg_state[i] becomes the state before segment i (in scan
 // order, from init), final_state the state behind the last one.
-cudaError_t launch_combine(const ScanArgs& a, cudaStream_t st);
+// One or two scans of a call in one launch.
+cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st);
 // dst[row][head][:] = sum over the `group` scan heads that share the head of src[row][head * group + g][:].
 cudaError_t launch_group_sum(const float* src, void* dst, int64_t rows, int heads, int group, int width, bool bf16,
                              cudaStream_t st);

@@ -21,18 +21,12 @@ template <int DKP> constexpr size_t smem_bytes() {
     return sizeof(float) * (2 * C * (DKP + 4) + C * PV + DKP * PV + C * PP + 3 * C);
 }
 
-template <typename T> __device__ __forceinline__ void load4(const T* p, float (&v)[4]);
-template <> __device__ __forceinline__ void load4<float>(const float* p, float (&v)[4]) {
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
     const float4 a = *reinterpret_cast<const float4*>(p);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
 }
-template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[4]) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xFFFF0000u);
-    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xFFFF0000u);
-}
 __device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ void sts4(float* p, float a, float b, float c, float d) {
+__device__ __forceinline__ void st4(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
 __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
@@ -42,7 +36,7 @@ __device__ __forceinline__ void axpy4(float (&o)[4], float a, float4 x) {
     o[0] = fmaf(a, x.x, o[0]); o[1] = fmaf(a, x.y, o[1]); o[2] = fmaf(a, x.z, o[2]); o[3] = fmaf(a, x.w, o[3]);
 }
 
-template <typename T, typename TO, int DKP, int MODE>
+template <int DKP, int MODE>
 __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PK = DKP + 4, TK = DKP / 16;  // state rows of a thread
@@ -68,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
     const float* init = MODE == kOutputs ? a.seg_state + ((size_t)blockIdx.x * a.H + h) * at_state
                         : MODE == kStates || !a.init ? nullptr
                                                      : a.init + ((size_t)g.seq * a.H + h) * at_state;
-    const bool init_t = MODE == kWhole && a.init_t;
+    const bool init_t = MODE == kWhole ? a.init_t : a.seg_t;
 #pragma unroll
     for (int r = 0; r < TK; ++r)
 #pragma unroll
@@ -78,10 +72,10 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
                           ? init[init_t ? (size_t)(dv0 + vv) * a.Dk + kk : (size_t)kk * a.Dv + dv0 + vv]
                           : 0.f;
         }
-    const T* q = static_cast<const T*>(a.q) + (size_t)(h / a.gq) * a.Dk;
-    const T* k = static_cast<const T*>(a.k) + (size_t)(h / a.gk) * a.Dk;
-    const T* v = static_cast<const T*>(a.v) + (size_t)(h / a.gv) * a.Dv + dv0;
-    TO* o = static_cast<TO*>(a.o) + (size_t)h * a.Dv + dv0;
+    const float* q = static_cast<const float*>(a.q) + (size_t)(h / a.gq) * a.Dk;
+    const float* k = static_cast<const float*>(a.k) + (size_t)(h / a.gk) * a.Dk;
+    const float* v = static_cast<const float*>(a.v) + (size_t)(h / a.gv) * a.Dv + dv0;
+    float* o = static_cast<float*>(a.o) + (size_t)h * a.Dv + dv0;
 
     for (int64_t c0 = 0; c0 < g.n; c0 += C) {
         const int n = (int)min((int64_t)C, g.n - c0);
@@ -91,23 +85,23 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
             const int r = i / (DKP / 4), d = (i % (DKP / 4)) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
             if (r < n && d < a.Dk) {
-                if (MODE != kStates) load4<T>(q + row(r) * a.rs_q + d, x);
-                load4<T>(k + row(r) * a.rs_k + d, y);
+                if (MODE != kStates) load4(q + row(r) * a.rs_q + d, x);
+                load4(k + row(r) * a.rs_k + d, y);
             }
-            if (MODE != kStates) sts4(sQ + r * PK + d, x[0], x[1], x[2], x[3]);
-            sts4(sK + r * PK + d, y[0], y[1], y[2], y[3]);
+            if (MODE != kStates) st4(sQ + r * PK + d, x[0], x[1], x[2], x[3]);
+            st4(sK + r * PK + d, y[0], y[1], y[2], y[3]);
         }
         for (int i = tid; i < C * (DVB / 4); i += kThreads) {
             const int r = i / (DVB / 4), d = (i % (DVB / 4)) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < n && d < nv) load4<T>(v + row(r) * a.rs_v + d, x);
-            sts4(sV + r * PV + d, x[0], x[1], x[2], x[3]);
+            if (r < n && d < nv) load4(v + row(r) * a.rs_v + d, x);
+            st4(sV + r * PV + d, x[0], x[1], x[2], x[3]);
         }
         if (MODE != kStates) {
 #pragma unroll
             for (int r = 0; r < TK; ++r) {
-                sts4(sS + (k0 + r) * PV + v0, S[r][0], S[r][1], S[r][2], S[r][3]);
-                sts4(sS + (k0 + r) * PV + v0 + 4, S[r][4], S[r][5], S[r][6], S[r][7]);
+                st4(sS + (k0 + r) * PV + v0, S[r][0], S[r][1], S[r][2], S[r][3]);
+                st4(sS + (k0 + r) * PV + v0 + 4, S[r][4], S[r][5], S[r][6], S[r][7]);
             }
         }
         __syncthreads();
@@ -167,9 +161,9 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
             for (int i = 0; i < 4; ++i) {
                 if (r0 + i < n && c4 < nv) {
                     const float e = a.inter_scale * sPow[r0 + i + s];
-                    TO* dst = o + row(r0 + i) * (int64_t)a.H * a.Dv + c4;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) dst[c] = from_f32<TO>(fmaf(e, in[i][c], out[i][c]));
+                    float* dst = o + row(r0 + i) * (int64_t)a.H * a.Dv + c4;
+                    st4(dst, fmaf(e, in[i][0], out[i][0]), fmaf(e, in[i][1], out[i][1]), fmaf(e, in[i][2], out[i][2]),
+                         fmaf(e, in[i][3], out[i][3]));
                 }
             }
         }
@@ -204,35 +198,34 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
     }
 }
 
-template <typename T, typename TO, int DKP, int MODE>
+template <int DKP, int MODE>
 cudaError_t launch(const ScanArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(scan_simt_kernel<T, TO, DKP, MODE>,
+    cudaError_t e = cudaFuncSetAttribute(scan_simt_kernel<DKP, MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DKP>());
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.seg_len ? a.slots : a.batch), a.H, (a.Dv + DVB - 1) / DVB);
-    scan_simt_kernel<T, TO, DKP, MODE><<<grid, kThreads, smem_bytes<DKP>(), st>>>(a);
+    scan_simt_kernel<DKP, MODE><<<grid, kThreads, smem_bytes<DKP>(), st>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T, typename TO, int MODE>
+template <int MODE>
 cudaError_t launch_dk(const ScanArgs& a, cudaStream_t st) {
-    if (a.Dk <= 32) return launch<T, TO, 32, MODE>(a, st);
-    if (a.Dk <= 64) return launch<T, TO, 64, MODE>(a, st);
-    return launch<T, TO, 128, MODE>(a, st);
+    if (a.Dk <= 32) return launch<32, MODE>(a, st);
+    if (a.Dk <= 64) return launch<64, MODE>(a, st);
+    return launch<128, MODE>(a, st);
 }
 
 }  // namespace
 
-template <typename T, typename TO>
-static cudaError_t launch_mode(const ScanArgs& a, Mode mode, cudaStream_t st) {
-    if (mode == kStates) return launch_dk<T, TO, kStates>(a, st);
-    return mode == kOutputs ? launch_dk<T, TO, kOutputs>(a, st) : launch_dk<T, TO, kWhole>(a, st);
-}
-
-cudaError_t launch_scan_simt(const ScanArgs& a, Mode mode, cudaStream_t st) {
-    if (a.bf16) return a.o_f32 ? launch_mode<__nv_bfloat16, float>(a, mode, st)
-                               : launch_mode<__nv_bfloat16, __nv_bfloat16>(a, mode, st);
-    return launch_mode<float, float>(a, mode, st);
+cudaError_t launch_scan_simt(const ScanArgs* scans, int count, Mode mode, cudaStream_t st) {
+    for (int i = 0; i < count; ++i) {
+        const ScanArgs& a = scans[i];
+        const cudaError_t e = mode == kStates    ? launch_dk<kStates>(a, st)
+                              : mode == kOutputs ? launch_dk<kOutputs>(a, st)
+                                                 : launch_dk<kWhole>(a, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace la

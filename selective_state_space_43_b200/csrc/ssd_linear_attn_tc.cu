@@ -17,7 +17,7 @@
 // chunk before.
 //
 // Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself
-// stays fp32); o once.  V' is split into kTerms bf16 parts (v w = hi + mid + lo, each the rounding of what the parts
+// stays fp32); o once.  V' is split into bf16 parts (v w = hi + mid + lo, each the rounding of what the parts
 // before leave): 3 parts carry 24 bits, so a state that the caller gets is as exact as fp32 sums; 2 parts
 // (17 bits) where S only feeds bf16 outputs.
 //
@@ -56,9 +56,15 @@ enum Bar { FULL = 0, EMPTY = 2, PFULL = 4, PREADY = 6, VREADY = 8, DSFULL, SREAD
 // TMEM columns: scores (two buffers; their bf16 form overlays each half), Y1, Y2, dS (two buffers)
 constexpr uint32_t COL_P = 0, COL_Y1 = 256, COL_Y2 = 320, COL_DS = 384;
 
-struct Params {
+// Up to three scans in one launch (a gradient's), their blocks one behind the other.
+constexpr int kMaxScans = 3;
+struct Scan {
     CUtensorMap tq, tk, tv;
     ScanArgs a;
+    unsigned blocks;
+};
+struct Params {
+    Scan scan[kMaxScans];
 };
 
 // Moves registers between warpgroups: of the 768 x 80 launched with, 2 x 128 x 24 go to the scores, given by
@@ -158,10 +164,14 @@ __device__ __forceinline__ void store16(float* p, const float (&v)[16], int n, b
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// kMode: see Mode.  kTerms: bf16 parts of V'.  TO: type of the outputs.
-template <int kMode, int kTerms, typename TO>
+// kMode: see Mode.
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ Params prm) {
-    const ScanArgs& a = prm.a;
+    int which = 0;
+    unsigned block = blockIdx.x;
+    while (block >= prm.scan[which].blocks) block -= prm.scan[which++].blocks;
+    const Scan& scan = prm.scan[which];
+    const ScanArgs& a = scan.a;
     uint8_t* sm = ssd_la_smem + ((1024u - (smem_u32(ssd_la_smem) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
     volatile int* stop = reinterpret_cast<volatile int*>(sm + OFF_BAR + 200);
@@ -170,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int ndvb = (a.Dv + DVB - 1) / DVB;
-    const int dv0 = (int)(blockIdx.x % ndvb) * DVB;
-    const int h = (int)(blockIdx.x / ndvb % a.H);
-    const int64_t slot = blockIdx.x / ((unsigned)ndvb * a.H);
+    const int dv0 = (int)(block % ndvb) * DVB;
+    const int h = (int)(block / ndvb % a.H);
+    const int64_t slot = block / ((unsigned)ndvb * a.H);
     const Segment g = segment_of(a, slot);
     if (a.cu && a.seg_len == 0 && tid == 0 && h == 0 && dv0 == 0 && !sequence_span(a, slot).ok)
         atomicOr(a.err, kErrBadSeqlens);
@@ -202,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
+    // parts of V': see the top of the file
+    const int terms = kMode == kStates || (kMode == kWhole && a.final_state) ? 3 : 2;
     const float l = a.log_decay[h];
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
@@ -220,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 if (s) last1 = c;
                 else last0 = c;
                 for (int b = 0; b < boxes; ++b) {
-                    tma_load_3d(st + OFF_K + b * kBox, &prm.tk, &bars[FULL + s], b * 64, h / a.gk, r);
-                    if (kOut) tma_load_3d(st + b * kBox, &prm.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                    tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                    if (kOut) tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
                 }
-                tma_load_3d(st + OFF_V, &prm.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
             }
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
             if (last0 >= 0) mbar_wait(&bars[FULL], (last0 >> 1) & 1, nullptr, 100000000ull);
@@ -265,8 +277,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8 * kTerms; ++k)  // V' parts lie behind one another: 8 steps are a box
+                    for (int k = 0; k < 16; ++k)  // V' parts lie behind one another: 8 steps are a box
                         mma_bf16(tmem + COL_DS + s * 64, dKt + (k & 7) * 128, dVP + k * 128, ID_DS, k > 0);
+                    if (terms == 3) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16(tmem + COL_DS + s * 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS, 1);
+                    }
                     mma_commit(&bars[DSFULL]);
                 }
                 __syncwarp();
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const float* init = kMode == kOutputs ? a.seg_state + ((size_t)slot * a.H + h) * size
                             : kMode == kStates || !a.init ? nullptr
                                                           : a.init + ((size_t)g.seq * a.H + h) * size;
-        const bool init_t = kMode == kWhole && a.init_t;
+        const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
 #pragma unroll
         for (int d = 0; d < kHalf; ++d)
             S[d] = init && row < a.Dk && d < nh
@@ -396,21 +413,22 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const uint32_t o = sw128_off(row, half * 4 + i);
                 const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
                 const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                uint32_t part[kTerms][4];
+                uint32_t part[3][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f0 = bf_lo(in[k]) * w, f1 = bf_hi(in[k]) * w;
 #pragma unroll
-                    for (int t = 0; t < kTerms; ++t) {
+                    for (int t = 0; t < 3; ++t) {
                         part[t][k] = pack_bf2(f0, f1);
                         f0 -= bf_lo(part[t][k]);
                         f1 -= bf_hi(part[t][k]);
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-                    *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
-                        make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
+                for (int t = 0; t < 3; ++t)
+                    if (t < 2 || terms == 3)
+                        *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
+                            make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
             }
             fence_async_smem();
             warp_arrive(&bars[VREADY], lane);
@@ -464,13 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
             const float e_full = coefficient(C);
             // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
-            const bool wide = a.Dv * sizeof(TO) % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+            const int esize = a.o_f32 ? 4 : 2;
+            const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
             for (int c = 0; c < nc; ++c) {
                 const int n = chunk_n(c);
                 const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
                 if (!warp_wait(&bars[YFULL], c & 1, stop)) { *stop = 1; break; }
                 tc_fence_after();
-                TO* dst = static_cast<TO*>(a.o) + (chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0;
+                uint8_t* dst = static_cast<uint8_t*>(a.o) +
+                               ((chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0) * esize;
                 const int live = row < n ? nv : 0;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -484,7 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) x[j] = fmaf(e, y[j], x[j]);
-                    store16(dst + b * 16, x, live - b * 16, wide);
+                    if (a.o_f32)
+                        store16(reinterpret_cast<float*>(dst) + b * 16, x, live - b * 16, wide);
+                    else
+                        store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, live - b * 16, wide);
                 }
             }
         }
@@ -526,30 +549,33 @@ bool make_map(CUtensorMap* m, const void* base, int width, int heads, int64_t ro
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kMode, int kTerms, typename TO> cudaError_t launch(const Params& prm, cudaStream_t st) {
-    static const cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kMode, kTerms, TO>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+template <int kMode> cudaError_t launch(const Params& prm, unsigned blocks, cudaStream_t st) {
+    static const cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    const ScanArgs& a = prm.a;
-    const int64_t blocks = (a.seg_len ? a.slots : a.batch) * a.H * ((a.Dv + DVB - 1) / DVB);
-    scan_tc_kernel<kMode, kTerms, TO><<<(unsigned)blocks, kThreads, kSmemBytes, st>>>(prm);
+    scan_tc_kernel<kMode><<<blocks, kThreads, kSmemBytes, st>>>(prm);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_scan_tc(const ScanArgs& a, Mode mode, cudaStream_t st) {
+cudaError_t launch_scan_tc(const ScanArgs* scans, int count, Mode mode, cudaStream_t st) {
     Params prm;
-    prm.a = a;
-    if (a.rows > 0 && (!make_map(&prm.tk, a.k, a.Dk, a.H / a.gk, a.rows, a.rs_k) ||
-                       !make_map(&prm.tv, a.v, a.Dv, a.H / a.gv, a.rows, a.rs_v) ||
-                       !make_map(&prm.tq, a.q, a.Dk, a.H / a.gq, a.rows, a.rs_q)))
-        return cudaErrorInvalidValue;
-    using bf16 = __nv_bfloat16;
-    if (mode == kStates) return launch<kStates, 3, bf16>(prm, st);
-    if (mode == kOutputs) return a.o_f32 ? launch<kOutputs, 2, float>(prm, st) : launch<kOutputs, 2, bf16>(prm, st);
-    if (a.final_state) return a.o_f32 ? launch<kWhole, 3, float>(prm, st) : launch<kWhole, 3, bf16>(prm, st);
-    return a.o_f32 ? launch<kWhole, 2, float>(prm, st) : launch<kWhole, 2, bf16>(prm, st);
+    unsigned blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        const ScanArgs& a = scans[i];
+        Scan& s = prm.scan[i];
+        s.a = a;
+        s.blocks = (unsigned)((a.seg_len ? a.slots : a.batch) * a.H * ((a.Dv + DVB - 1) / DVB));
+        blocks += s.blocks;
+        if (a.rows > 0 && (!make_map(&s.tk, a.k, a.Dk, a.H / a.gk, a.rows, a.rs_k) ||
+                           !make_map(&s.tv, a.v, a.Dv, a.H / a.gv, a.rows, a.rs_v) ||
+                           (mode != kStates && !make_map(&s.tq, a.q, a.Dk, a.H / a.gq, a.rows, a.rs_q))))
+            return cudaErrorInvalidValue;
+    }
+    if (blocks == 0) return cudaSuccess;
+    if (mode == kStates) return launch<kStates>(prm, blocks, st);
+    return mode == kOutputs ? launch<kOutputs>(prm, blocks, st) : launch<kWhole>(prm, blocks, st);
 }
 
 }  // namespace la

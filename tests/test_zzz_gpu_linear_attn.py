@@ -266,7 +266,8 @@ def test_bad_offsets_are_reported(dtype):
             ops.device_status()
         ops.device_status()  # reading clears it
         if cu[1] == 100 and cu[0] == 0:
-            # the valid sequences are computed; rows 90 .. 99 belong to two of them in the first list
+            # short enough not to be cut into segments, so the valid sequences are computed; rows 90 .. 99 belong to two
+            # of them in the first list
             assert torch.equal(o[:90], good[0][:90]) and torch.equal(S[0], good[1][0])
 
 
@@ -348,3 +349,71 @@ def test_a_small_workspace_is_replaced_and_wrong_tensors_are_refused():
         ops.linear_attn_prefill(x["q"].transpose(1, 2), x["k"], x["v"], x["log_decay"])
     with pytest.raises(ops.SsdError):
         ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"], o=x["q"])
+
+
+def workspace_bytes(L, H, Hk, dk, dv, dtype, packed=False, B=1, backward=False):
+    import ctypes
+    f = ops.lib().ssd_linear_attn_backward_workspace_bytes if backward else ops.lib().ssd_linear_attn_prefill_workspace_bytes
+    return f(ctypes.byref(ops.SsdLinearAttnDims(B, L, H, Hk, dk, dv)), 1 if dtype == torch.bfloat16 else 0, packed)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("L,Hk,group,dk,dv,init", [(2500, 2, 1, 64, 128, True), (4096, 1, 2, 128, 64, False),
+                                                   (3333, 1, 1, 96, 40, True)])
+def test_long_sequences_in_segments(L, Hk, group, dk, dv, init, dtype):
+    """Few heads on a long sequence: the sequence axis is cut (the workspace holds the segments' states)."""
+    H = Hk * group
+    assert workspace_bytes(L, H, Hk, dk, dv, dtype) > 0
+    x = make(L, (1, L), H, Hk, dk, dv, dtype, init=init, grads=True)
+    x["log_decay"][0] = -1e-4  # one head remembers across every segment
+    o, S = ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"], x["init"])
+    got = ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["d_final"])
+    ops.device_status()
+    wo, wS, mo, mS = lo.prefill(x["q"], x["k"], x["v"], x["log_decay"], dk ** -0.5, x["init"])
+    check_out(o, wo, mo, dtype, L, dk, "o")
+    check_state(S, wS, mS, L, dk, "final_state")
+    want, mag = lo.backward(x["q"], x["k"], x["v"], x["log_decay"], dk ** -0.5, x["do"], x["init"], x["d_final"])
+    for name in "qkv":
+        check_out(got[name], want[name], mag[name], dtype, L, max(dk, dv), "d" + name)
+    check_state(got["init_state"], want["init_state"], mag["init_state"], L, max(dk, dv), "d_init_state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cu", [[0, 0, 1500, 1501, 4000], [5, 261, 2821, 2821, 3077, 4001], [0, 4000]])
+def test_packed_segments(cu, dtype):
+    T, n, H, Hk, dk, dv = cu[-1] + 70, len(cu) - 1, 2, 1, 64, 64
+    assert workspace_bytes(T, H, Hk, dk, dv, dtype, True, n) > 0
+    x = make(sum(cu), (T,), H, Hk, dk, dv, dtype, nseq=n, init=True, grads=True)
+    x["log_decay"][0] = -3e-4
+    for name in ("q", "k", "v", "do"):
+        x[name][cu[-1]:] = float("nan")
+        x[name][:cu[0]] = float("nan")
+    o = torch.full((T, H, dv), 7.0, dtype=dtype, device="cuda")
+    o, S = ops.linear_attn_prefill_varlen(x["q"], x["k"], x["v"], x["log_decay"], cu, x["init"], o=o)
+    got = ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["d_final"],
+                                   cu_seqlens=cu)
+    ops.device_status()
+    assert (o[cu[-1]:] == 7).all() and (o[:cu[0]] == 7).all()
+    clean = {k: None if v is None else torch.nan_to_num(v, 0, 0, 0) for k, v in x.items()}
+    wo, wS, mo, mS = lo.prefill(clean["q"], clean["k"], clean["v"], x["log_decay"], 0.125, x["init"], cu)
+    check_out(o, wo, mo, dtype, 4000, dk, "o")
+    check_state(S, wS, mS, 4000, dk, "final_state")
+    want, mag = lo.backward(clean["q"], clean["k"], clean["v"], x["log_decay"], 0.125, clean["do"], x["init"],
+                            x["d_final"], cu)
+    for name in "qkv":
+        check_out(got[name], want[name], mag[name], dtype, 4000, dk, "d" + name)
+    check_state(got["init_state"], want["init_state"], mag["init_state"], 4000, dk, "d_init_state")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_bad_offsets_in_segments(dtype):
+    x = make(1, (4000,), 2, 2, 64, 64, dtype, nseq=3, init=True, grads=True)
+    for cu in ([0, 3000, 2000, 4000], [0, 2000, 3000, 4001], [-1, 100, 100, 4000], [0, 1 << 60, 100, 4000],
+               [4000, 0, 4000, 0]):
+        ops.linear_attn_prefill_varlen(x["q"], x["k"], x["v"], x["log_decay"], cu, x["init"])
+        with pytest.raises(ops.SsdError):
+            ops.device_status()
+        ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["d_final"], cu_seqlens=cu)
+        with pytest.raises(ops.SsdError):
+            ops.device_status()
+        ops.device_status()
