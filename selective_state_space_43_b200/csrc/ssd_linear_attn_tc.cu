@@ -17,9 +17,9 @@
 // chunk before.
 //
 // Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself
-// stays fp32); o once.  V' is split into bf16 parts (v w = hi + mid + lo, each the rounding of what the parts
-// before leave): 3 parts carry 24 bits, so a state that the caller gets is as exact as fp32 sums; 2 parts
-// (17 bits) where S only feeds bf16 outputs.
+// stays fp32); o once.  V' is cut into bf16 parts of 8 bits
+// (v w = hi + mid + lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits) where what the second leaves
+// would show in a state that the caller gets, so that such a state is as exact as fp32 sums.
 //
 // 24 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
@@ -52,9 +52,10 @@ constexpr uint32_t OFF_VP = 2 * kStage;          // V': up to three boxes
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
 constexpr uint32_t kSmemBytes = OFF_BAR + 256 + 1024;  // + alignment of the base
-enum Bar { FULL = 0, EMPTY = 2, PFULL = 4, PREADY = 6, VREADY = 8, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, kBars };
-// TMEM columns: scores (two buffers; their bf16 form overlays each half), Y1, Y2, dS (two buffers)
-constexpr uint32_t COL_P = 0, COL_Y1 = 256, COL_Y2 = 320, COL_DS = 384;
+// KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
+enum Bar { FULL = 0, KFREE = 2, QFREE = 4, VFREE = 6, PFULL = 8, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, kBars };
+// TMEM columns: scores (their bf16 form overlays each half), Y1, Y2, dS (two buffers of two parts)
+constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
 
 // Up to three scans in one launch (a gradient's), their blocks one behind the other.
 constexpr int kMaxScans = 3;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], i == PREADY || i == PREADY + 1 || i == VREADY || i == SREADY ? 8 : i == EPI ? 4 : 1);
+                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY ? 8 : i == EPI ? 4 : 1);
             *stop = 0;
             fence_mbar_init();
         }
@@ -212,9 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // parts of V': see the top of the file
-    const int terms = kMode == kStates || (kMode == kWhole && a.final_state) ? 3 : 2;
     const float l = a.log_decay[h];
+    // Whether V' of chunk c needs its third part: what the second leaves (2^-16) still shows in a state that the
+    // caller gets, e^{l d} after d more rows.
+    const bool exact = kMode == kStates || (kMode == kWhole && a.final_state);
+    auto third = [&](int c) { return exact && l * (float)(rev ? (int64_t)(nc - 1 - c) * C : g.n - (int64_t)(c + 1) * C) > -6.f; };
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
 
@@ -224,18 +227,24 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             int last0 = -1, last1 = -1;  // last chunk loaded into each stage
             const int boxes = a.Dk > 64 ? 2 : 1;
             for (int c = 0; c < nc; ++c) {
-                const int s = c & 1;
-                if (c >= 2 && !mbar_wait(&bars[EMPTY + s], ((c >> 1) - 1) & 1, stop)) { *stop = 1; break; }
+                const int s = c & 1, r = (int)chunk_row(c);
+                const uint32_t old = ((c >> 1) - 1) & 1;
                 uint8_t* st = sm + s * kStage;
-                const int r = (int)chunk_row(c);
+                bool ok = c < 2 || mbar_wait(&bars[KFREE + s], old, stop);
                 mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
+                // each tile as soon as its place is free (and in any case: the bytes are expected)
+                for (int b = 0; b < boxes; ++b)
+                    tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                if (kOut) {
+                    ok = ok && (c < 2 || mbar_wait(&bars[QFREE + s], old, stop));
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                }
+                ok = ok && (c < 2 || mbar_wait(&bars[VFREE + s], old, stop));
+                tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
                 if (s) last1 = c;
                 else last0 = c;
-                for (int b = 0; b < boxes; ++b) {
-                    tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
-                    if (kOut) tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
-                }
-                tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                if (!ok) { *stop = 1; break; }
             }
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
             if (last0 >= 0) mbar_wait(&bars[FULL], (last0 >> 1) & 1, nullptr, 100000000ull);
@@ -245,84 +254,75 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             // The whole warp runs this loop, so that descriptors stay in uniform registers; one elected lane issues.
             constexpr uint32_t ID_P = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t ID_Y = idesc_bf16_f32(128, 64, false, true);
-            constexpr uint32_t ID_DS = idesc_bf16_f32(128, 64, true, true);
+            constexpr uint32_t ID_DS = idesc_bf16_f32(128, 128, true, true), ID_DS3 = idesc_bf16_f32(128, 64, true, true);
             uint32_t base = smem_u32(sm);
-            auto scores = [&](int c) {  // P(c) = Q K^T
-                const uint32_t st = base + (c & 1) * kStage, d = tmem + COL_P + (c & 1) * 128;
-                const uint64_t dQ = sw128_desc(st, 16, 1024), dK = sw128_desc(st + OFF_K, 16, 1024);
-                if (elect_one()) {
-                    mma_k64<false>(d, dQ, dK, ID_P, 0);
-                    if (a.Dk > 64) mma_k64<false>(d, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
-                    mma_commit(&bars[PFULL + (c & 1)]);
-                }
-                __syncwarp();
-            };
-            int issued = 0;  // chunks whose scores are under way
             for (int c = 0; c < nc; ++c) {
                 const int s = c & 1;
                 // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
                 // of being kept (and spilled) over the loop
                 asm volatile("" : "+r"(base));
                 const uint32_t st = base + s * kStage;
-                const uint64_t dVP = sw128_desc(base + OFF_VP, 16384, 1024), dS = sw128_desc(base + OFF_S, 16384, 1024);
-                if (kOut && issued <= c) {
-                    if (!warp_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
-                    tc_fence_after();
-                    scores(c);
-                    issued = c + 1;
+                const uint64_t dQ = sw128_desc(st, 16, 1024);
+                if (!warp_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                tc_fence_after();
+                if (kOut) {  // P = Q K^T (the product that read the scores before was issued before)
+                    const uint64_t dK = sw128_desc(st + OFF_K, 16, 1024);
+                    if (elect_one()) {
+                        mma_k64<false>(tmem + COL_P, dQ, dK, ID_P, 0);
+                        if (a.Dk > 64) mma_k64<false>(tmem + COL_P, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
+                        mma_commit(&bars[PFULL]);
+                    }
+                    __syncwarp();
                 }
-                // dS(c) = K^T V' (V' is written after the tiles have landed)
+                // dS = K^T V' (its buffer was read before the S that the last Y2 waited for): the parts lie one box
+                // behind the other, the first two are one product with 64 columns each, so that K is read once; the third
+                // adds to the second
                 if (!warp_wait(&bars[VREADY], c & 1, stop)) { *stop = 1; break; }
                 tc_fence_after();
-                const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024);
+                const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)  // V' parts lie behind one another: 8 steps are a box
-                        mma_bf16(tmem + COL_DS + s * 64, dKt + (k & 7) * 128, dVP + k * 128, ID_DS, k > 0);
-                    if (terms == 3) {
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16(tmem + COL_DS + s * 128, dKt + k * 128, dVP + k * 128, ID_DS, k > 0);
+                    if (third(c)) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16(tmem + COL_DS + s * 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS, 1);
+                            mma_bf16(tmem + COL_DS + s * 128 + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
                     }
                     mma_commit(&bars[DSFULL]);
+                    mma_commit(&bars[KFREE + s]);
                 }
                 __syncwarp();
                 if (kOut) {
-                    // Y2(c) = Q S, once S is written and the chunk before has been read out
+                    // Y2 = Q S, once S is written and the outputs before have been read
                     if (!warp_wait(&bars[SREADY], c & 1, stop) ||
                         (c >= 1 && !warp_wait(&bars[EPI], (c - 1) & 1, stop))) {
                         *stop = 1;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t dQ = sw128_desc(st, 16, 1024);
+                    const uint64_t dS = sw128_desc(base + OFF_S, 16384, 1024);
                     if (elect_one()) {
                         mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 0);
                         if (a.Dk > 64) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
                         mma_commit(&bars[Y2DONE]);
+                        mma_commit(&bars[QFREE + s]);
                     }
                     __syncwarp();
-                    // the next chunk's scores, if its tiles are here already (never waited for: this chunk's
-                    // stage has to be freed for the load behind it)
-                    if (c + 1 < nc && __all_sync(0xffffffffu, mbar_test(&bars[FULL + (s ^ 1)], ((c + 1) >> 1) & 1))) {
-                        tc_fence_after();
-                        scores(c + 1);
-                        issued = c + 2;
-                    }
-                    // Y1(c) = P V
-                    if (!warp_wait(&bars[PREADY + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                    // Y1 = P V
+                    if (!warp_wait(&bars[PREADY], c & 1, stop)) { *stop = 1; break; }
                     tc_fence_after();
                     const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
-                    const uint32_t p = tmem + COL_P + s * 128;
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
-                            mma_bf16_ts(tmem + COL_Y1, p + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y, k > 0);
+                            mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y,
+                                        k > 0);
                         mma_commit(&bars[YFULL]);
                     }
                     __syncwarp();
                 }
-                if (elect_one()) mma_commit(&bars[EMPTY + s]);
+                if (elect_one()) mma_commit(&bars[VFREE + s]);
                 __syncwarp();
             }
             // nothing may still be running on the tensor cores when TMEM is released
@@ -342,27 +342,36 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 m[j] = far < 0 ? 0.f : far == 0 ? a.qk_scale : a.qk_scale * expf(l * (float)far);
             }
             for (int c = 0; c < nc; ++c) {
-                const int s = c & 1, n = chunk_n(c);
-                if (!warp_wait(&bars[PFULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
+                const int n = chunk_n(c);
+                if (!warp_wait(&bars[PFULL], c & 1, stop)) { *stop = 1; break; }
                 tc_fence_after();
-                const uint32_t col = lane_base + COL_P + s * 128 + j0;
+                const uint32_t col = lane_base + COL_P + j0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float v[16];
-                    uint32_t p[8];
-                    tmem_ld16(col + b * 16, v);
+                for (int b = 0; b < 4; b += 2) {
+                    float v[2][16];
+                    tmem_ld16(col + b * 16, v[0]);
+                    tmem_ld16(col + b * 16 + 16, v[1]);
                     tmem_wait_ld();
-                    if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = j0 + b * 16 + j < n ? v[j] : 0.f;
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t p[8];
+                        const int j1 = (b + i) * 16;
+                        if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[i][j] = j0 + j1 + j < n ? v[i][j] : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 f = __fmul2_rn(make_float2(v[i][2 * j], v[i][2 * j + 1]),
+                                                        make_float2(m[j1 + 2 * j], m[j1 + 2 * j + 1]));
+                            p[j] = pack_bf2(f.x, f.y);
+                        }
+                        tmem_st8(col + (b + i) * 8, p);  // over columns already read
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = pack_bf2(v[2 * j] * m[b * 16 + 2 * j], v[2 * j + 1] * m[b * 16 + 2 * j + 1]);
-                    tmem_st8(col + b * 8, p);  // over columns already read
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(&bars[PREADY + s], lane);
+                warp_arrive(&bars[PREADY], lane);
             }
         }
     } else if (warp < kWarpOut) {
@@ -397,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const float w_full = weight(C), decay_full = decay_pow(l, C);
         auto split = [&](int c) {  // V'(c), and zeros behind the sequence's end
             const int n = chunk_n(c);
+            const bool three = third(c);
             uint8_t* st = sm + (c & 1) * kStage;
             const float w = n == C ? w_full : row < n ? weight(n) : 0.f;
             if (row >= n) {
@@ -416,17 +426,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 uint32_t part[3][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float f0 = bf_lo(in[k]) * w, f1 = bf_hi(in[k]) * w;
+                    float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(w, w));
+                    // a part is the upper half of the word: 8 bits cut off, the rest exact
 #pragma unroll
                     for (int t = 0; t < 3; ++t) {
-                        part[t][k] = pack_bf2(f0, f1);
-                        f0 -= bf_lo(part[t][k]);
-                        f1 -= bf_hi(part[t][k]);
+                        const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
+                        part[t][k] = __byte_perm(x, y, 0x7632);
+                        if (t < 2) f = __fadd2_rn(f, make_float2(-bf_hi(x), -bf_hi(y)));
                     }
                 }
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
-                    if (t < 2 || terms == 3)
+                    if (t < 2 || three)
                         *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
                             make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
             }
@@ -441,28 +452,41 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         }
         for (int c = 0; ok && c < nc; ++c) {
             ok = warp_wait(&bars[DSFULL], c & 1, stop);
-            if (!ok) break;
-            if (c + 1 < nc) {  // the next V' first: its product runs while S is updated
-                ok = warp_wait(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1, stop);
-                if (!ok) break;
-                split(c + 1);
-            }
-            tc_fence_after();
-            const int n = chunk_n(c);
-            const float e = n == C ? decay_full : decay_pow(l, n);
+            // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
+            // here, so that its product runs while S is updated
+            const bool more = c + 1 < nc;
+            const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1));
+#pragma unroll 1
+            for (int step = 0; ok && step < 2; ++step) {
+                if ((step == 0) == ahead) {
+                    if (!more) continue;
+                    ok = warp_wait(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1, stop);
+                    if (ok) split(c + 1);
+                    continue;
+                }
+                tc_fence_after();
+                const int n = chunk_n(c);
+                const float e = n == C ? decay_full : decay_pow(l, n);
 #pragma unroll
-            for (int b = 0; b < kHalf / 16; ++b) {
-                float v[16];
-                tmem_ld16(lane_base + COL_DS + (c & 1) * 64 + half * kHalf + b * 16, v);
-                tmem_wait_ld();
+                for (int b = 0; b < kHalf / 16; ++b) {
+                    const uint32_t col = lane_base + COL_DS + (c & 1) * 128 + half * kHalf + b * 16;
+                    float x[16], y[16];
+                    tmem_ld16(col, x);
+                    tmem_ld16(col + 64, y);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[b * 16 + j] = fmaf(e, S[b * 16 + j], v[j]);
-            }
-            tc_fence_before();
-            if (kOut && c + 1 < nc) {
-                ok = warp_wait(&bars[Y2DONE], c & 1, stop);
-                if (!ok) break;
-                publish();
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
+                        const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 16 + j], S[b * 16 + j + 1]), d);
+                        S[b * 16 + j] = f.x;
+                        S[b * 16 + j + 1] = f.y;
+                    }
+                }
+                tc_fence_before();
+                if (kOut && more) {
+                    ok = warp_wait(&bars[Y2DONE], c & 1, stop);
+                    if (ok) publish();
+                }
             }
         }
         if (!ok) *stop = 1;
@@ -503,7 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         warp_arrive(&bars[EPI], lane);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = fmaf(e, y[j], x[j]);
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 f = __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
+                        x[j] = f.x;
+                        x[j + 1] = f.y;
+                    }
                     if (a.o_f32)
                         store16(reinterpret_cast<float*>(dst) + b * 16, x, live - b * 16, wide);
                     else
