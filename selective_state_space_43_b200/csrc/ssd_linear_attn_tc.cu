@@ -44,16 +44,17 @@ namespace {
 using namespace ssd::sm100;
 
 constexpr int C = 128, DVB = 64, kHalf = 32;
-constexpr int kWarpOut = 16, kWarpTma = 20, kWarpMma = 21, kThreads = 24 * 32;
+constexpr int kWarpOut = 16, kWarpTma = 20, kWarpMma = 21, kWarpItem = 22, kThreads = 24 * 32;
 constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
 constexpr uint32_t kStage = 5 * kBox;            // Q (2), K (2), V (1)
 constexpr uint32_t OFF_K = 2 * kBox, OFF_V = 4 * kBox;
 constexpr uint32_t OFF_VP = 2 * kStage;          // V': up to three boxes
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
-constexpr uint32_t kSmemBytes = OFF_BAR + 256 + 1024;  // + alignment of the base
+constexpr uint32_t OFF_ITEM = OFF_BAR + 256;
+constexpr uint32_t kSmemBytes = OFF_BAR + 512 + 1024;  // + alignment of the base
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
-enum Bar { FULL = 0, KFREE = 2, QFREE = 4, VFREE = 6, PFULL = 8, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, kBars };
+enum Bar { FULL = 0, KFREE = 2, QFREE = 4, VFREE = 6, PFULL = 8, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
 // TMEM columns: scores (their bf16 form overlays each half), Y1, Y2, dS (two buffers of two parts)
 constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
 
@@ -68,8 +69,9 @@ struct Params {
     Scan scan[kMaxScans];
 };
 
-// Moves registers between warpgroups: of the 768 x 80 launched with, 2 x 128 x 24 go to the scores, given by
-// V' and S (2 x 128 x 8), the outputs (128 x 8) and the last warpgroup (128 x 24).
+// Moves registers between warpgroups: of the 768 x 80 launched with, 2 x 128 x 32 go to the scores, given by
+// V' and S (2 x 128 x 8), the outputs (128 x 16) and the last warpgroup (128 x 32); where there are no scores,
+// V' and S take 24 of what the scores' warps (256 x 40) and the other two (128 x (16 + 32)) give.
 template <int N> __device__ __forceinline__ void regs_more() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -79,6 +81,18 @@ template <int N> __device__ __forceinline__ void regs_fewer() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop));
 }
+// A CTA's work: one (64 value channels, head, sequence or segment) behind the other.  The item warp announces
+// them in a ring of kItems places that the other roles read in the same order, each at its own pace.
+constexpr int kItems = 3;
+constexpr uint64_t kItemWait = 100000000000ull;  // 100 s: the longest item is a whole sequence
+struct Item {
+    int scan, h, dv0;  // scan < 0: no more
+    int slot, seq;
+    int row0, nc, last;  // first row, chunks, rows of the chunk that ends the sequence (or segment)
+    int third;           // the last chunks, in scan order, whose V' needs its third part
+    float l;
+};
+static_assert(sizeof(Item) * kItems <= 256, "the ring's place");
 // Whether the phase is complete, without waiting (try_wait suspends the thread for a while).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -165,43 +179,49 @@ __device__ __forceinline__ void store16(float* p, const float (&v)[16], int n, b
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Asks the hardware for a block of this grid that has not started (its 16-byte answer arrives on `bar`); the running
+// CTA then does that block's work and the block is never launched.
+__device__ __forceinline__ void ask_next_block(void* answer, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The block's index, or -1 when none is left.
+__device__ __forceinline__ int64_t next_block(const void* answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return got ? (int64_t)x : -1;
+}
+
 // kMode: see Mode.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ Params prm) {
-    int which = 0;
-    unsigned block = blockIdx.x;
-    while (block >= prm.scan[which].blocks) block -= prm.scan[which++].blocks;
-    const Scan& scan = prm.scan[which];
-    const ScanArgs& a = scan.a;
     uint8_t* sm = ssd_la_smem + ((1024u - (smem_u32(ssd_la_smem) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
     volatile int* stop = reinterpret_cast<volatile int*>(sm + OFF_BAR + 200);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_BAR + 208);
+    uint8_t* answer = sm + OFF_BAR + 224;
+    Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
     constexpr bool kOut = kMode != kStates;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int ndvb = (a.Dv + DVB - 1) / DVB;
-    const int dv0 = (int)(block % ndvb) * DVB;
-    const int h = (int)(block / ndvb % a.H);
-    const int64_t slot = block / ((unsigned)ndvb * a.H);
-    const Segment g = segment_of(a, slot);
-    if (a.cu && a.seg_len == 0 && tid == 0 && h == 0 && dv0 == 0 && !sequence_span(a, slot).ok)
-        atomicOr(a.err, kErrBadSeqlens);
-    if (!g.ok) return;
-    const int nv = min(DVB, a.Dv - dv0);
-    const int nc = (int)((g.n + C - 1) / C);
-    const bool rev = a.reverse;
-    // chunk c in scan order -> its first row and its rows
-    auto chunk_row = [&](int c) { return g.row0 + (int64_t)(rev ? nc - 1 - c : c) * C; };
-    auto chunk_n = [&](int c) {
-        const int64_t left = g.n - (int64_t)(rev ? nc - 1 - c : c) * C;
-        return left < C ? (int)left : C;
-    };
-
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY ? 8 : i == EPI ? 4 : 1);
+                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY ? 8
+                                    : i == EPI                                ? 4
+                                    : i >= IEMPTY                             ? (kOut ? 22 : 10)  // roles that read an item
+                                                                              : 1);
             *stop = 0;
             fence_mbar_init();
         }
@@ -213,183 +233,283 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const float l = a.log_decay[h];
-    // Whether V' of chunk c needs its third part: what the second leaves (2^-16) still shows in a state that the
-    // caller gets, e^{l d} after d more rows.
-    const bool exact = kMode == kStates || (kMode == kWhole && a.final_state);
-    auto third = [&](int c) { return exact && l * (float)(rev ? (int64_t)(nc - 1 - c) * C : g.n - (int64_t)(c + 1) * C) > -6.f; };
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
 
+    // A place of the ring, for a whole warp (lanes agree) or for one lane alone; nullptr: no more.  It is given back by
+    // leave(), after the role has copied what it needs.
+    auto enter = [&](int number, bool whole_warp) -> const Item* {
+        const int i = number % kItems;
+        bool ok = mbar_wait(&bars[IFULL + i], (number / kItems) & 1, stop, kItemWait);
+        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) *stop = 1;
+        return ok && items[i].scan >= 0 ? &items[i] : nullptr;
+    };
+    auto leave = [&](int number, bool whole_warp) {
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(&bars[IEMPTY + number % kItems]);
+    };
+    // the place of chunk c, in scan order, among the item's chunks; the rows of the chunk at a place
+    auto place_of = [](bool rev, int nc, int c) { return rev ? nc - 1 - c : c; };
+    auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };
+
     if (warp >= kWarpTma) {
-        regs_fewer<56>();
-        if (warp == kWarpTma && lane == 0) {
-            int last0 = -1, last1 = -1;  // last chunk loaded into each stage
-            const int boxes = a.Dk > 64 ? 2 : 1;
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1, r = (int)chunk_row(c);
-                const uint32_t old = ((c >> 1) - 1) & 1;
-                uint8_t* st = sm + s * kStage;
-                bool ok = c < 2 || mbar_wait(&bars[KFREE + s], old, stop);
-                mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
-                // each tile as soon as its place is free (and in any case: the bytes are expected)
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
-                if (kOut) {
-                    ok = ok && (c < 2 || mbar_wait(&bars[QFREE + s], old, stop));
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+        regs_fewer<48>();
+        if (warp == kWarpItem && lane == 0) {
+            // ---- items ----
+            int64_t block = blockIdx.x;
+            int put = 0;
+            auto announce = [&](const Item& it) {
+                const int i = put % kItems;
+                if (put >= kItems && !mbar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
+                items[i] = it;
+                mbar_arrive(&bars[IFULL + i]);
+                ++put;
+                return true;
+            };
+            for (int asked = 0;; ++asked) {
+                Item it;
+                it.scan = 0;
+                unsigned b = (unsigned)block;
+                while (b >= prm.scan[it.scan].blocks) b -= prm.scan[it.scan++].blocks;
+                const ScanArgs& a = prm.scan[it.scan].a;
+                const unsigned ndvb = (a.Dv + DVB - 1) / DVB;
+                it.dv0 = (int)(b % ndvb) * DVB;
+                it.h = (int)(b / ndvb % a.H);
+                it.slot = (int)(b / (ndvb * (unsigned)a.H));
+                const Segment g = segment_of(a, it.slot);
+                if (a.cu && a.seg_len == 0 && it.h == 0 && it.dv0 == 0 && !sequence_span(a, it.slot).ok)
+                    atomicOr(a.err, kErrBadSeqlens);
+                it.seq = (int)g.seq;
+                it.row0 = (int)g.row0;
+                it.nc = (int)((g.n + C - 1) / C);
+                it.last = (int)(g.n - (int64_t)(it.nc - 1) * C);
+                it.l = a.log_decay[it.h];
+                // What the second part leaves (2^-16) shows in a state that the caller gets unless at least d rows follow
+                // with e^{l d} < 2^-8: l d < -6.
+                it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
+                           : it.l < 0.f ? (int)fminf(6.f / (C * -it.l) + 2.f, 1e9f)
+                                        : 1 << 30;
+                // the next block is taken only when this item's last loads are due, so that none waits here while
+                // another SM is idle
+                bool ok = !g.ok || (announce(it) && mbar_wait(&bars[LASTLOAD], (put - 1) & 1, stop, kItemWait));
+                if (ok) {
+                    mbar_arrive_expect_tx(&bars[NEXT], 16);
+                    ask_next_block(answer, &bars[NEXT]);
+                    ok = mbar_wait(&bars[NEXT], asked & 1, nullptr);
+                    block = next_block(answer);
+                    fence_async_smem();  // read before the next answer is written
                 }
-                ok = ok && (c < 2 || mbar_wait(&bars[VFREE + s], old, stop));
-                tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
-                if (s) last1 = c;
-                else last0 = c;
-                if (!ok) { *stop = 1; break; }
+                if (!ok) *stop = 1;
+                if (!ok || block < 0) break;
+            }
+            Item end;
+            end.scan = -1;
+            if (!announce(end)) *stop = 1;
+        } else if (warp == kWarpTma && lane == 0) {
+            // ---- tile loads; cc counts the CTA's chunks over all its items ----
+            int cc = 0;
+            const Item* it;
+            for (int k = 0; !*stop && (it = enter(k, false)) != nullptr; ++k) {
+                const Scan& scan = prm.scan[it->scan];
+                const ScanArgs& a = scan.a;
+                const int h = it->h, dv0 = it->dv0, nc = it->nc, row0 = it->row0;
+                const bool rev = a.reverse;
+                leave(k, false);
+                const int boxes = a.Dk > 64 ? 2 : 1;
+                if (nc == 0) mbar_arrive(&bars[LASTLOAD]);
+                for (int c = 0; c < nc; ++c, ++cc) {
+                    if (c == nc - 1) mbar_arrive(&bars[LASTLOAD]);
+                    const int s = cc & 1, r = row0 + place_of(rev, nc, c) * C;
+                    const uint32_t old = ((cc >> 1) - 1) & 1;
+                    uint8_t* st = sm + s * kStage;
+                    bool ok = cc < 2 || mbar_wait(&bars[KFREE + s], old, stop);
+                    mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
+                    // each tile as soon as its place is free (and in any case: the bytes are expected)
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                    if (kOut) {
+                        ok = ok && (cc < 2 || mbar_wait(&bars[QFREE + s], old, stop));
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                    }
+                    ok = ok && (cc < 2 || mbar_wait(&bars[VFREE + s], old, stop));
+                    tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                    if (!ok) {
+                        *stop = 1;
+                        ++cc;
+                        break;
+                    }
+                }
             }
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
-            if (last0 >= 0) mbar_wait(&bars[FULL], (last0 >> 1) & 1, nullptr, 100000000ull);
-            if (last1 >= 0) mbar_wait(&bars[FULL + 1], (last1 >> 1) & 1, nullptr, 100000000ull);
-        }
-        if (warp == kWarpMma) {
-            // The whole warp runs this loop, so that descriptors stay in uniform registers; one elected lane issues.
+            if (cc > 0) mbar_wait(&bars[FULL + ((cc - 1) & 1)], ((cc - 1) >> 1) & 1, nullptr, 100000000ull);
+            if (cc > 1) mbar_wait(&bars[FULL + (cc & 1)], ((cc - 2) >> 1) & 1, nullptr, 100000000ull);
+        } else if (warp == kWarpMma) {
+            // ---- products.  The whole warp runs this loop, so that descriptors stay in uniform registers; one elected
+            // lane issues.
             constexpr uint32_t ID_P = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t ID_Y = idesc_bf16_f32(128, 64, false, true);
             constexpr uint32_t ID_DS = idesc_bf16_f32(128, 128, true, true), ID_DS3 = idesc_bf16_f32(128, 64, true, true);
             uint32_t base = smem_u32(sm);
-            for (int c = 0; c < nc; ++c) {
-                const int s = c & 1;
-                // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
-                // of being kept (and spilled) over the loop
-                asm volatile("" : "+r"(base));
-                const uint32_t st = base + s * kStage;
-                const uint64_t dQ = sw128_desc(st, 16, 1024);
-                if (!warp_wait(&bars[FULL + s], (c >> 1) & 1, stop)) { *stop = 1; break; }
-                tc_fence_after();
-                if (kOut) {  // P = Q K^T (the product that read the scores before was issued before)
-                    const uint64_t dK = sw128_desc(st + OFF_K, 16, 1024);
-                    if (elect_one()) {
-                        mma_k64<false>(tmem + COL_P, dQ, dK, ID_P, 0);
-                        if (a.Dk > 64) mma_k64<false>(tmem + COL_P, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
-                        mma_commit(&bars[PFULL]);
+            int cc = 0;
+            const Item* it;
+            bool ok = true;
+            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+                const bool wide = prm.scan[it->scan].a.Dk > 64;
+                const int nc = it->nc, third = it->third;
+                leave(k, true);
+                for (int c = 0; ok && c < nc; ++c, ++cc) {
+                    const int s = cc & 1;
+                    // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
+                    // of being kept (and spilled) over the loop
+                    asm volatile("" : "+r"(base));
+                    const uint32_t st = base + s * kStage;
+                    const uint64_t dQ = sw128_desc(st, 16, 1024);
+                    if (!(ok = warp_wait(&bars[FULL + s], (cc >> 1) & 1, stop))) break;
+                    tc_fence_after();
+                    if (kOut) {  // P = Q K^T (the product that read the scores before was issued before)
+                        const uint64_t dK = sw128_desc(st + OFF_K, 16, 1024);
+                        if (elect_one()) {
+                            mma_k64<false>(tmem + COL_P, dQ, dK, ID_P, 0);
+                            if (wide) mma_k64<false>(tmem + COL_P, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
+                            mma_commit(&bars[PFULL]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                // dS = K^T V' (its buffer was read before the S that the last Y2 waited for): the parts lie one box
-                // behind the other, the first two are one product with 64 columns each, so that K is read once; the third
-                // adds to the second
-                if (!warp_wait(&bars[VREADY], c & 1, stop)) { *stop = 1; break; }
-                tc_fence_after();
-                const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16(tmem + COL_DS + s * 128, dKt + k * 128, dVP + k * 128, ID_DS, k > 0);
-                    if (third(c)) {
+                    // dS = K^T V' (its buffer was read before the S that the last Y2 waited for): the parts lie one box
+                    // behind the other, the first two are one product with 64 columns each, so that K is read once; the
+                    // third adds to the second
+                    if (!(ok = warp_wait(&bars[VREADY], cc & 1, stop))) break;
+                    tc_fence_after();
+                    const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16(tmem + COL_DS + s * 128 + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
-                    }
-                    mma_commit(&bars[DSFULL]);
-                    mma_commit(&bars[KFREE + s]);
-                }
-                __syncwarp();
-                if (kOut) {
-                    // Y2 = Q S, once S is written and the outputs before have been read
-                    if (!warp_wait(&bars[SREADY], c & 1, stop) ||
-                        (c >= 1 && !warp_wait(&bars[EPI], (c - 1) & 1, stop))) {
-                        *stop = 1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t dS = sw128_desc(base + OFF_S, 16384, 1024);
-                    if (elect_one()) {
-                        mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 0);
-                        if (a.Dk > 64) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
-                        mma_commit(&bars[Y2DONE]);
-                        mma_commit(&bars[QFREE + s]);
-                    }
-                    __syncwarp();
-                    // Y1 = P V
-                    if (!warp_wait(&bars[PREADY], c & 1, stop)) { *stop = 1; break; }
-                    tc_fence_after();
-                    const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
-                    if (elect_one()) {
+                            mma_bf16(tmem + COL_DS + s * 128, dKt + k * 128, dVP + k * 128, ID_DS, k > 0);
+                        if (nc - c <= third) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
-                            mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y,
-                                        k > 0);
-                        mma_commit(&bars[YFULL]);
+                            for (int k = 0; k < 8; ++k)
+                                mma_bf16(tmem + COL_DS + s * 128 + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
+                        }
+                        mma_commit(&bars[DSFULL]);
+                        mma_commit(&bars[KFREE + s]);
                     }
                     __syncwarp();
+                    if (kOut) {
+                        // Y2 = Q S, once S is written and the outputs before have been read
+                        ok = warp_wait(&bars[SREADY], cc & 1, stop) && (cc == 0 || warp_wait(&bars[EPI], (cc - 1) & 1, stop));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dS = sw128_desc(base + OFF_S, 16384, 1024);
+                        if (elect_one()) {
+                            mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 0);
+                            if (wide) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
+                            mma_commit(&bars[Y2DONE]);
+                            mma_commit(&bars[QFREE + s]);
+                        }
+                        __syncwarp();
+                        // Y1 = P V
+                        if (!(ok = warp_wait(&bars[PREADY], cc & 1, stop))) break;
+                        tc_fence_after();
+                        const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
+                                mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y,
+                                            k > 0);
+                            mma_commit(&bars[YFULL]);
+                        }
+                        __syncwarp();
+                    }
+                    if (elect_one()) mma_commit(&bars[VFREE + s]);
+                    __syncwarp();
                 }
-                if (elect_one()) mma_commit(&bars[VFREE + s]);
-                __syncwarp();
             }
+            if (!ok) *stop = 1;
             // nothing may still be running on the tensor cores when TMEM is released
             if (elect_one()) mma_commit(&bars[MMADONE]);
             __syncwarp();
             mbar_wait(&bars[MMADONE], 0, nullptr, 100000000ull);
         }
     } else if (warp < 8) {
-        regs_more<104>();
-        if (kOut) {
+        if (!kOut) {
+            regs_fewer<40>();
+        } else {
+            regs_more<112>();
             // ---- scores: row `row`, columns 64 half .. 64 half + 63 ----
             const int j0 = (warp >> 2) * 64;
-            float m[64];
+            int cc = 0;
+            const Item* it;
+            bool ok = true;
+            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+                const ScanArgs& a = prm.scan[it->scan].a;
+                const int nc = it->nc, last = it->last;
+                const float l = it->l;
+                const bool rev = a.reverse;
+                leave(k, true);
+                // one factor e^l per step away from the diagonal (off by 127 fp32 roundings at most, far below bf16's)
+                float m[64];
+                const float el = decay_pow(l, 1);
+                // distance of the half's column nearest the diagonal: the last one, against the time the first
+                const int near = rev ? j0 - row : row - (j0 + 63);
+                float cur = near > 0 ? a.qk_scale * decay_pow(l, near) : 0.f;
+                auto next = [&](int i) {  // the factor i columns from there; 0 until the diagonal is reached
+                    if (near + i == 0) cur = a.qk_scale;
+                    else if (i > 0) cur *= el;
+                    return cur;
+                };
+                if (rev) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-                const int far = rev ? j0 + j - row : row - (j0 + j);
-                m[j] = far < 0 ? 0.f : far == 0 ? a.qk_scale : a.qk_scale * expf(l * (float)far);
-            }
-            for (int c = 0; c < nc; ++c) {
-                const int n = chunk_n(c);
-                if (!warp_wait(&bars[PFULL], c & 1, stop)) { *stop = 1; break; }
-                tc_fence_after();
-                const uint32_t col = lane_base + COL_P + j0;
+                    for (int i = 0; i < 64; ++i) m[i] = next(i);
+                } else {
 #pragma unroll
-                for (int b = 0; b < 4; b += 2) {
-                    float v[2][16];
-                    tmem_ld16(col + b * 16, v[0]);
-                    tmem_ld16(col + b * 16 + 16, v[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t p[8];
-                        const int j1 = (b + i) * 16;
-                        if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[i][j] = j0 + j1 + j < n ? v[i][j] : 0.f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 f = __fmul2_rn(make_float2(v[i][2 * j], v[i][2 * j + 1]),
-                                                        make_float2(m[j1 + 2 * j], m[j1 + 2 * j + 1]));
-                            p[j] = pack_bf2(f.x, f.y);
-                        }
-                        tmem_st8(col + (b + i) * 8, p);  // over columns already read
-                    }
+                    for (int i = 0; i < 64; ++i) m[63 - i] = next(i);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bars[PREADY], lane);
+                for (int c = 0; ok && c < nc; ++c, ++cc) {
+                    const int n = rows_of(place_of(rev, nc, c), nc, last);
+                    if (!(ok = warp_wait(&bars[PFULL], cc & 1, stop))) break;
+                    tc_fence_after();
+                    const uint32_t col = lane_base + COL_P + j0;
+#pragma unroll
+                    for (int b = 0; b < 4; b += 2) {
+                        float v[2][16];
+                        tmem_ld16(col + b * 16, v[0]);
+                        tmem_ld16(col + b * 16 + 16, v[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t p[8];
+                            const int j1 = (b + i) * 16;
+                            if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[i][j] = j0 + j1 + j < n ? v[i][j] : 0.f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 f = __fmul2_rn(make_float2(v[i][2 * j], v[i][2 * j + 1]),
+                                                            make_float2(m[j1 + 2 * j], m[j1 + 2 * j + 1]));
+                                p[j] = pack_bf2(f.x, f.y);
+                            }
+                            tmem_st8(col + (b + i) * 8, p);  // over columns already read
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&bars[PREADY], lane);
+                }
             }
+            if (!ok) *stop = 1;
         }
     } else if (warp < kWarpOut) {
         // ---- V' and S: tile row / key row `row`, 32 of the 64 channels ----
-        regs_fewer<72>();
-        const int half = (warp >> 2) & 1, d0 = dv0 + half * kHalf;
-        const int nh = min(kHalf, a.Dv - d0);
+        if (kOut) regs_fewer<72>();
+        else regs_more<104>();
+        const int half = (warp >> 2) & 1;
         float S[kHalf];
-        const size_t size = (size_t)a.Dk * a.Dv;
-        const float* init = kMode == kOutputs ? a.seg_state + ((size_t)slot * a.H + h) * size
-                            : kMode == kStates || !a.init ? nullptr
-                                                          : a.init + ((size_t)g.seq * a.H + h) * size;
-        const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
-#pragma unroll
-        for (int d = 0; d < kHalf; ++d)
-            S[d] = init && row < a.Dk && d < nh
-                       ? init[init_t ? (size_t)(d0 + d) * a.Dk + row : (size_t)row * a.Dv + d0 + d]
-                       : 0.f;
+        int cc = 0;
+        const Item* it;
+        bool ok = true;
         auto publish = [&] {  // the bf16 copy that Y2 reads
             uint8_t* p = sm + OFF_S;
 #pragma unroll
@@ -400,151 +520,183 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             fence_async_smem();
             warp_arrive(&bars[SREADY], lane);
         };
-        auto weight = [&](int n) {  // of tile row `row` in the state behind a chunk of n rows
-            return a.w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row);
-        };
-        const float w_full = weight(C), decay_full = decay_pow(l, C);
-        auto split = [&](int c) {  // V'(c), and zeros behind the sequence's end
-            const int n = chunk_n(c);
-            const bool three = third(c);
-            uint8_t* st = sm + (c & 1) * kStage;
-            const float w = n == C ? w_full : row < n ? weight(n) : 0.f;
-            if (row >= n) {
+        for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+            const ScanArgs& a = prm.scan[it->scan].a;
+            const int nc = it->nc, last = it->last, third = it->third;
+            const float l = it->l;
+            const bool rev = a.reverse;
+            const int d0 = it->dv0 + half * kHalf;
+            // the state's place among the sequences' or the segments'
+            const int state = (kMode == kWhole ? it->seq : it->slot) * a.H + it->h;
+            leave(k, true);
+            {
+                const float* init = kMode == kOutputs ? a.seg_state : kMode == kStates ? nullptr : a.init;
+                const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
+                const float* p = init + (size_t)state * a.Dk * a.Dv + (init_t ? (size_t)d0 * a.Dk + row : (size_t)row * a.Dv + d0);
+                const int step = init_t ? a.Dk : 1;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t o = sw128_off(row, i);
-                    const uint4 z = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(st + OFF_K + half * kBox + o) = z;
-                    if (i / 4 == half) *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
-                }
+                for (int d = 0; d < kHalf; ++d) S[d] = init && row < a.Dk && d0 + d < a.Dv ? p[d * step] : 0.f;
             }
+            auto weight = [&](int n) {  // of tile row `row` in the state behind a chunk of n rows
+                return a.w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row);
+            };
+            const float w_full = weight(C), decay_full = decay_pow(l, C);
+            auto split = [&](int c, int s) {  // V' of chunk c, in stage s; zeros behind the sequence's end
+                const int n = rows_of(place_of(rev, nc, c), nc, last);
+                const bool three = nc - c <= third;
+                uint8_t* st = sm + s * kStage;
+                const float wr = n == C ? w_full : row < n ? weight(n) : 0.f;
+                if (row >= n) {
 #pragma unroll
-            for (int i = 0; i < kHalf / 8; ++i) {
-                const uint32_t o = sw128_off(row, half * 4 + i);
-                const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
-                const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                uint32_t part[3][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(w, w));
-                    // a part is the upper half of the word: 8 bits cut off, the rest exact
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) {
-                        const uint32_t x = __float_as_uint(f.x), y = __float_as_uint(f.y);
-                        part[t][k] = __byte_perm(x, y, 0x7632);
-                        if (t < 2) f = __fadd2_rn(f, make_float2(-bf_hi(x), -bf_hi(y)));
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t o = sw128_off(row, i);
+                        const uint4 z = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(st + OFF_K + half * kBox + o) = z;
+                        if (i / 4 == half) *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
-                    if (t < 2 || three)
-                        *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
-                            make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
-            }
-            fence_async_smem();
-            warp_arrive(&bars[VREADY], lane);
-        };
-        bool ok = true;
-        if (nc > 0) {
-            if (kOut) publish();
-            ok = warp_wait(&bars[FULL], 0, stop);
-            if (ok) split(0);
-        }
-        for (int c = 0; ok && c < nc; ++c) {
-            ok = warp_wait(&bars[DSFULL], c & 1, stop);
-            // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
-            // here, so that its product runs while S is updated
-            const bool more = c + 1 < nc;
-            const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1));
-#pragma unroll 1
-            for (int step = 0; ok && step < 2; ++step) {
-                if ((step == 0) == ahead) {
-                    if (!more) continue;
-                    ok = warp_wait(&bars[FULL + ((c + 1) & 1)], ((c + 1) >> 1) & 1, stop);
-                    if (ok) split(c + 1);
-                    continue;
-                }
-                tc_fence_after();
-                const int n = chunk_n(c);
-                const float e = n == C ? decay_full : decay_pow(l, n);
+                for (int i = 0; i < kHalf / 8; ++i) {
+                    const uint32_t o = sw128_off(row, half * 4 + i);
+                    const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t part[3][4];
 #pragma unroll
-                for (int b = 0; b < kHalf / 16; ++b) {
-                    const uint32_t col = lane_base + COL_DS + (c & 1) * 128 + half * kHalf + b * 16;
-                    float x[16], y[16];
-                    tmem_ld16(col, x);
-                    tmem_ld16(col + 64, y);
-                    tmem_wait_ld();
+                    for (int k = 0; k < 4; ++k) {
+                        float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(wr, wr));
+                        // a part is the upper half of the word: 8 bits cut off, the rest exact
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
-                        const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 16 + j], S[b * 16 + j + 1]), d);
-                        S[b * 16 + j] = f.x;
-                        S[b * 16 + j + 1] = f.y;
+                        for (int t = 0; t < 3; ++t) {
+                            const uint32_t x0 = __float_as_uint(f.x), x1 = __float_as_uint(f.y);
+                            part[t][k] = __byte_perm(x0, x1, 0x7632);
+                            if (t < 2) f = __fadd2_rn(f, make_float2(-bf_hi(x0), -bf_hi(x1)));
+                        }
                     }
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+                        if (t < 2 || three)
+                            *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
+                                make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
                 }
-                tc_fence_before();
-                if (kOut && more) {
-                    ok = warp_wait(&bars[Y2DONE], c & 1, stop);
+                fence_async_smem();
+                warp_arrive(&bars[VREADY], lane);
+            };
+            if (nc > 0) {
+                if (kOut) {  // over the S that the item before left, once it has been read
+                    ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
                     if (ok) publish();
                 }
+                ok = ok && warp_wait(&bars[FULL + (cc & 1)], (cc >> 1) & 1, stop);
+                if (ok) split(0, cc & 1);
+            }
+            for (int c = 0; ok && c < nc; ++c, ++cc) {
+                if (!(ok = warp_wait(&bars[DSFULL], cc & 1, stop))) break;
+                // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
+                // here, so that its product runs while S is updated
+                const bool more = c + 1 < nc;
+                const uint32_t s1 = (cc + 1) & 1, par1 = ((cc + 1) >> 1) & 1;
+                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + s1], par1));
+#pragma unroll 1
+                for (int step = 0; ok && step < 2; ++step) {
+                    if ((step == 0) == ahead) {
+                        if (!more) continue;
+                        ok = warp_wait(&bars[FULL + s1], par1, stop);
+                        if (ok) split(c + 1, s1);
+                        continue;
+                    }
+                    tc_fence_after();
+                    const int n = rows_of(place_of(rev, nc, c), nc, last);
+                    const float e = n == C ? decay_full : decay_pow(l, n);
+#pragma unroll
+                    for (int b = 0; b < kHalf / 16; ++b) {
+                        const uint32_t col = lane_base + COL_DS + (cc & 1) * 128 + half * kHalf + b * 16;
+                        float x[16], y[16];
+                        tmem_ld16(col, x);
+                        tmem_ld16(col + 64, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
+                            const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 16 + j], S[b * 16 + j + 1]), d);
+                            S[b * 16 + j] = f.x;
+                            S[b * 16 + j + 1] = f.y;
+                        }
+                    }
+                    tc_fence_before();
+                    if (kOut && more) {
+                        ok = warp_wait(&bars[Y2DONE], cc & 1, stop);
+                        if (ok) publish();
+                    }
+                }
+            }
+            float* fin = kMode == kOutputs ? nullptr : kMode == kStates ? a.seg_state : a.final_state;
+            if (ok && fin && row < a.Dk) {
+                float* p = fin + (size_t)state * a.Dk * a.Dv + (size_t)row * a.Dv + d0;
+#pragma unroll
+                for (int d = 0; d < kHalf; d += 4)
+                    if (d0 + d < a.Dv) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
             }
         }
         if (!ok) *stop = 1;
-        float* fin = kMode == kStates  ? a.seg_state + ((size_t)slot * a.H + h) * size
-                     : kMode == kWhole ? (a.final_state ? a.final_state + ((size_t)g.seq * a.H + h) * size : nullptr)
-                                       : nullptr;
-        if (ok && fin && row < a.Dk) {
-            float* p = fin + (size_t)row * a.Dv + d0;
-#pragma unroll
-            for (int d = 0; d < kHalf; d += 4)
-                if (d < nh) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
-        }
     } else {
-        regs_fewer<72>();
+        regs_fewer<64>();
         if (kOut) {
             // ---- outputs: tile row `row` ----
-            auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
-            const float e_full = coefficient(C);
-            // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
-            const int esize = a.o_f32 ? 4 : 2;
-            const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
-            for (int c = 0; c < nc; ++c) {
-                const int n = chunk_n(c);
-                const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
-                if (!warp_wait(&bars[YFULL], c & 1, stop)) { *stop = 1; break; }
-                tc_fence_after();
-                uint8_t* dst = static_cast<uint8_t*>(a.o) +
-                               ((chunk_row(c) + row) * (int64_t)a.H * a.Dv + (int64_t)h * a.Dv + dv0) * esize;
-                const int live = row < n ? nv : 0;
+            int cc = 0;
+            const Item* it;
+            bool ok = true;
+            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+                const ScanArgs& a = prm.scan[it->scan].a;
+                const int nc = it->nc, last = it->last, nv = min(DVB, a.Dv - it->dv0);
+                const float l = it->l;
+                const bool rev = a.reverse;
+                const int64_t row_elems = (int64_t)a.H * a.Dv;
+                const int64_t first = ((int64_t)it->row0 + row) * row_elems + (int64_t)it->h * a.Dv + it->dv0;
+                leave(k, true);
+                auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
+                const float e_full = coefficient(C);
+                // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
+                const int esize = a.o_f32 ? 4 : 2;
+                const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+                for (int c = 0; ok && c < nc; ++c, ++cc) {
+                    const int place = place_of(rev, nc, c), n = rows_of(place, nc, last);
+                    const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
+                    if (!(ok = warp_wait(&bars[YFULL], cc & 1, stop))) break;
+                    tc_fence_after();
+                    uint8_t* dst = static_cast<uint8_t*>(a.o) + (first + (int64_t)place * C * row_elems) * esize;
+                    const int live = row < n ? nv : 0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float x[16], y[16];
-                    tmem_ld16(lane_base + COL_Y1 + b * 16, x);
-                    tmem_ld16(lane_base + COL_Y2 + b * 16, y);
-                    tmem_wait_ld();
-                    if (b == 3) {
-                        tc_fence_before();
-                        warp_arrive(&bars[EPI], lane);
-                    }
+                    for (int b = 0; b < 4; ++b) {
+                        float x[16], y[16];
+                        tmem_ld16(lane_base + COL_Y1 + b * 16, x);
+                        tmem_ld16(lane_base + COL_Y2 + b * 16, y);
+                        tmem_wait_ld();
+                        if (b == 3) {
+                            tc_fence_before();
+                            warp_arrive(&bars[EPI], lane);
+                        }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 f = __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
-                        x[j] = f.x;
-                        x[j + 1] = f.y;
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 f =
+                                __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
+                            x[j] = f.x;
+                            x[j + 1] = f.y;
+                        }
+                        if (a.o_f32)
+                            store16(reinterpret_cast<float*>(dst) + b * 16, x, live - b * 16, wide);
+                        else
+                            store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, live - b * 16, wide);
                     }
-                    if (a.o_f32)
-                        store16(reinterpret_cast<float*>(dst) + b * 16, x, live - b * 16, wide);
-                    else
-                        store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, live - b * 16, wide);
                 }
             }
+            if (!ok) *stop = 1;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
-    if (tid == 0 && *stop) atomicOr(a.err, kErrTimeout);
+    if (tid == 0 && *stop) atomicOr(prm.scan[0].a.err, kErrTimeout);
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
