@@ -26,7 +26,7 @@
 //   8-15  V' of the next chunk (shared memory -> shared memory), then S of this one (TMEM -> registers ->
 //         shared memory), 32 channels each; the same threads zero the rows behind a sequence's end in K and V
 //   16-19 o: TMEM -> registers -> global, a row per thread in 32-byte stores
-//   20    TMA: Q, K, V of a chunk, two stages
+//   20    TMA: K, V, Q of a chunk, two or three stages
 //   21    tcgen05.mma (22 and 23 only complete the warpgroup)
 // Bound by HBM where there are enough heads: Q, K, V are read once (Q and K once for each 64 value
 // channels, the second time from L2), o written once.
@@ -46,15 +46,16 @@ using namespace ssd::sm100;
 constexpr int C = 128, DVB = 64, kHalf = 32;
 constexpr int kWarpOut = 16, kWarpTma = 20, kWarpMma = 21, kWarpItem = 22, kThreads = 24 * 32;
 constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
-constexpr uint32_t kStage = 5 * kBox;            // Q (2), K (2), V (1)
-constexpr uint32_t OFF_K = 2 * kBox, OFF_V = 4 * kBox;
-constexpr uint32_t OFF_VP = 2 * kStage;          // V': up to three boxes
+constexpr uint32_t OFF_VP = 10 * kBox;           // behind the stages; V': up to three boxes
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
-constexpr uint32_t OFF_ITEM = OFF_BAR + 256;
+constexpr uint32_t OFF_STOP = OFF_BAR + 240, OFF_TMEM = OFF_BAR + 248, OFF_ANSWER = OFF_BAR + 256, OFF_ITEM = OFF_BAR + 288;
 constexpr uint32_t kSmemBytes = OFF_BAR + 512 + 1024;  // + alignment of the base
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
-enum Bar { FULL = 0, KFREE = 2, QFREE = 4, VFREE = 6, PFULL = 8, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
+constexpr int kStages = 3;  // at most
+enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, PFULL = 12, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE,
+           NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
+static_assert(kBars * 8 <= 240, "the barriers' place");
 // TMEM columns: scores (their bf16 form overlays each half), Y1, Y2, dS (two buffers of two parts)
 constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
 
@@ -92,7 +93,31 @@ struct Item {
     int third;           // the last chunks, in scan order, whose V' needs its third part
     float l;
 };
-static_assert(sizeof(Item) * kItems <= 256, "the ring's place");
+static_assert(sizeof(Item) * kItems <= 512 - 288, "the ring's place");
+// The ring of tile stages, as each role follows it.  A stage is the K boxes (one per 64 of Dk), the V box and the Q
+// boxes of a chunk: three boxes or fewer leave room for three stages, Q and K of Dk > 64 for two.  Where the next
+// item's stages are cut differently the ring starts over at stage 0, when the loads have seen all others out.
+struct Ring {
+    int s = 0, kb = 0, count = 0;  // stage, K boxes, stages
+    uint32_t phases = 0;           // a bit for each stage
+    __device__ __forceinline__ bool cut(int Dk, bool q) {  // whether the cut changed
+        const int k = Dk > 64 ? 2 : 1;
+        if (k == kb) return false;
+        kb = k;
+        count = (q && k == 2) ? 2 : 3;
+        s = 0;
+        return true;
+    }
+    __device__ __forceinline__ uint32_t phase() const { return (phases >> s) & 1; }
+    __device__ __forceinline__ int after() const { return s + 1 == count ? 0 : s + 1; }
+    __device__ __forceinline__ void step() {
+        phases ^= 1u << s;
+        s = after();
+    }
+    __device__ __forceinline__ uint32_t k(bool q) const { return (uint32_t)s * (kb + 1 + (q ? kb : 0)) * kBox; }
+    __device__ __forceinline__ uint32_t v(bool q) const { return k(q) + kb * kBox; }
+    __device__ __forceinline__ uint32_t q(bool has) const { return v(has) + kBox; }
+};
 // Whether the phase is complete, without waiting (try_wait suspends the thread for a while).
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -208,11 +233,12 @@ template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ Params prm) {
     uint8_t* sm = ssd_la_smem + ((1024u - (smem_u32(ssd_la_smem) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
-    volatile int* stop = reinterpret_cast<volatile int*>(sm + OFF_BAR + 200);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_BAR + 208);
-    uint8_t* answer = sm + OFF_BAR + 224;
+    volatile int* stop = reinterpret_cast<volatile int*>(sm + OFF_STOP);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
+    uint8_t* answer = sm + OFF_ANSWER;
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
     constexpr bool kOut = kMode != kStates;
+    constexpr int kMaxParts = kMode == kOutputs ? 2 : 3;  // of V'
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (warp == kWarpMma) {
@@ -307,44 +333,43 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             end.scan = -1;
             if (!announce(end)) *stop = 1;
         } else if (warp == kWarpTma && lane == 0) {
-            // ---- tile loads; cc counts the CTA's chunks over all its items ----
-            int cc = 0;
+            // ---- tile loads ----
+            Ring ring;
             const Item* it;
+            // a place's products are complete (at once where there were none)
+            auto freed = [&](int bar, int i) { return mbar_wait(&bars[bar + i], ((ring.phases >> i) & 1) ^ 1, stop); };
             for (int k = 0; !*stop && (it = enter(k, false)) != nullptr; ++k) {
                 const Scan& scan = prm.scan[it->scan];
                 const ScanArgs& a = scan.a;
                 const int h = it->h, dv0 = it->dv0, nc = it->nc, row0 = it->row0;
                 const bool rev = a.reverse;
                 leave(k, false);
-                const int boxes = a.Dk > 64 ? 2 : 1;
+                bool ok = true;
+                if (ring.cut(a.Dk, kOut))
+                    for (int i = 0; i < kStages; ++i)
+                        ok = ok && freed(KFREE, i) && (!kOut || freed(QFREE, i)) && freed(VFREE, i);
                 if (nc == 0) mbar_arrive(&bars[LASTLOAD]);
-                for (int c = 0; c < nc; ++c, ++cc) {
+                for (int c = 0; ok && c < nc; ++c) {
                     if (c == nc - 1) mbar_arrive(&bars[LASTLOAD]);
-                    const int s = cc & 1, r = row0 + place_of(rev, nc, c) * C;
-                    const uint32_t old = ((cc >> 1) - 1) & 1;
-                    uint8_t* st = sm + s * kStage;
-                    bool ok = cc < 2 || mbar_wait(&bars[KFREE + s], old, stop);
-                    mbar_arrive_expect_tx(&bars[FULL + s], ((kOut ? 2 : 1) * boxes + 1) * kBox);
+                    const int s = ring.s, r = row0 + place_of(rev, nc, c) * C;
+                    ok = freed(KFREE, s);
+                    mbar_arrive_expect_tx(&bars[FULL + s], (ring.kb + 1 + (kOut ? ring.kb : 0)) * kBox);
                     // each tile as soon as its place is free (and in any case: the bytes are expected)
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_3d(st + OFF_K + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                    for (int b = 0; b < ring.kb; ++b)
+                        tma_load_3d(sm + ring.k(kOut) + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
                     if (kOut) {
-                        ok = ok && (cc < 2 || mbar_wait(&bars[QFREE + s], old, stop));
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_3d(st + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                        ok = ok && freed(QFREE, s);
+                        for (int b = 0; b < ring.kb; ++b)
+                            tma_load_3d(sm + ring.q(kOut) + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
                     }
-                    ok = ok && (cc < 2 || mbar_wait(&bars[VFREE + s], old, stop));
-                    tma_load_3d(st + OFF_V, &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
-                    if (!ok) {
-                        *stop = 1;
-                        ++cc;
-                        break;
-                    }
+                    ok = ok && freed(VFREE, s);
+                    tma_load_3d(sm + ring.v(kOut), &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                    ring.step();
                 }
+                if (!ok) *stop = 1;
             }
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
-            if (cc > 0) mbar_wait(&bars[FULL + ((cc - 1) & 1)], ((cc - 1) >> 1) & 1, nullptr, 100000000ull);
-            if (cc > 1) mbar_wait(&bars[FULL + (cc & 1)], ((cc - 2) >> 1) & 1, nullptr, 100000000ull);
+            for (int i = 0; i < kStages; ++i) mbar_wait(&bars[FULL + i], ((ring.phases >> i) & 1) ^ 1, nullptr, 100000000ull);
         } else if (warp == kWarpMma) {
             // ---- products.  The whole warp runs this loop, so that descriptors stay in uniform registers; one elected
             // lane issues.
@@ -352,24 +377,26 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             constexpr uint32_t ID_Y = idesc_bf16_f32(128, 64, false, true);
             constexpr uint32_t ID_DS = idesc_bf16_f32(128, 128, true, true), ID_DS3 = idesc_bf16_f32(128, 64, true, true);
             uint32_t base = smem_u32(sm);
-            int cc = 0;
+            int cc = 0;  // the CTA's chunks over all its items
+            Ring ring;
             const Item* it;
             bool ok = true;
             for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
-                const bool wide = prm.scan[it->scan].a.Dk > 64;
+                ring.cut(prm.scan[it->scan].a.Dk, kOut);
+                const bool wide = ring.kb == 2;
                 const int nc = it->nc, third = it->third;
                 leave(k, true);
-                for (int c = 0; ok && c < nc; ++c, ++cc) {
-                    const int s = cc & 1;
+                for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
+                    const int s = ring.s;
                     // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
                     // of being kept (and spilled) over the loop
                     asm volatile("" : "+r"(base));
-                    const uint32_t st = base + s * kStage;
-                    const uint64_t dQ = sw128_desc(st, 16, 1024);
-                    if (!(ok = warp_wait(&bars[FULL + s], (cc >> 1) & 1, stop))) break;
+                    const uint32_t tk = base + ring.k(kOut), tv = base + ring.v(kOut), ds = tmem + COL_DS + (cc & 1) * 128;
+                    const uint64_t dQ = sw128_desc(base + ring.q(kOut), 16, 1024);
+                    if (!(ok = warp_wait(&bars[FULL + s], ring.phase(), stop))) break;
                     tc_fence_after();
                     if (kOut) {  // P = Q K^T (the product that read the scores before was issued before)
-                        const uint64_t dK = sw128_desc(st + OFF_K, 16, 1024);
+                        const uint64_t dK = sw128_desc(tk, 16, 1024);
                         if (elect_one()) {
                             mma_k64<false>(tmem + COL_P, dQ, dK, ID_P, 0);
                             if (wide) mma_k64<false>(tmem + COL_P, dQ + (kBox >> 4), dK + (kBox >> 4), ID_P, 1);
@@ -382,15 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     // third adds to the second
                     if (!(ok = warp_wait(&bars[VREADY], cc & 1, stop))) break;
                     tc_fence_after();
-                    const uint64_t dKt = sw128_desc(st + OFF_K, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
+                    const uint64_t dKt = sw128_desc(tk, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16(tmem + COL_DS + s * 128, dKt + k * 128, dVP + k * 128, ID_DS, k > 0);
-                        if (nc - c <= third) {
+                            mma_bf16(ds, dKt + k * 128, dVP + k * 128, ID_DS, k > 0);
+                        if (kMaxParts == 3 && nc - c <= third) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                mma_bf16(tmem + COL_DS + s * 128 + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
+                                mma_bf16(ds + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
                         }
                         mma_commit(&bars[DSFULL]);
                         mma_commit(&bars[KFREE + s]);
@@ -412,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         // Y1 = P V
                         if (!(ok = warp_wait(&bars[PREADY], cc & 1, stop))) break;
                         tc_fence_after();
-                        const uint64_t dV = sw128_desc(st + OFF_V, 16384, 1024);
+                        const uint64_t dV = sw128_desc(tv, 16384, 1024);
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
@@ -508,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         const int half = (warp >> 2) & 1;
         float S[kHalf];
         int cc = 0;
+        Ring ring;
         const Item* it;
         bool ok = true;
         auto publish = [&] {  // the bf16 copy that Y2 reads
@@ -525,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const int nc = it->nc, last = it->last, third = it->third;
             const float l = it->l;
             const bool rev = a.reverse;
+            ring.cut(a.Dk, kOut);
             const int d0 = it->dv0 + half * kHalf;
             // the state's place among the sequences' or the segments'
             const int state = (kMode == kWhole ? it->seq : it->slot) * a.H + it->h;
@@ -541,39 +570,39 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 return a.w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row);
             };
             const float w_full = weight(C), decay_full = decay_pow(l, C);
-            auto split = [&](int c, int s) {  // V' of chunk c, in stage s; zeros behind the sequence's end
+            auto split = [&](int c, const Ring& at) {  // V' of chunk c; zeros behind the sequence's end
                 const int n = rows_of(place_of(rev, nc, c), nc, last);
-                const bool three = nc - c <= third;
-                uint8_t* st = sm + s * kStage;
+                const bool three = kMaxParts == 3 && nc - c <= third;
+                uint8_t* tv = sm + at.v(kOut);
                 const float wr = n == C ? w_full : row < n ? weight(n) : 0.f;
                 if (row >= n) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t o = sw128_off(row, i);
                         const uint4 z = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(st + OFF_K + half * kBox + o) = z;
-                        if (i / 4 == half) *reinterpret_cast<uint4*>(st + OFF_V + o) = z;
+                        if (half < at.kb) *reinterpret_cast<uint4*>(sm + at.k(kOut) + half * kBox + o) = z;
+                        if (i / 4 == half) *reinterpret_cast<uint4*>(tv + o) = z;
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kHalf / 8; ++i) {
                     const uint32_t o = sw128_off(row, half * 4 + i);
-                    const uint4 x = *reinterpret_cast<const uint4*>(st + OFF_V + o);
+                    const uint4 x = *reinterpret_cast<const uint4*>(tv + o);
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t part[3][4];
+                    uint32_t part[kMaxParts][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(wr, wr));
                         // a part is the upper half of the word: 8 bits cut off, the rest exact
 #pragma unroll
-                        for (int t = 0; t < 3; ++t) {
+                        for (int t = 0; t < kMaxParts; ++t) {
                             const uint32_t x0 = __float_as_uint(f.x), x1 = __float_as_uint(f.y);
                             part[t][k] = __byte_perm(x0, x1, 0x7632);
-                            if (t < 2) f = __fadd2_rn(f, make_float2(-bf_hi(x0), -bf_hi(x1)));
+                            if (t + 1 < kMaxParts) f = __fadd2_rn(f, make_float2(-bf_hi(x0), -bf_hi(x1)));
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)
+                    for (int t = 0; t < kMaxParts; ++t)
                         if (t < 2 || three)
                             *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
                                 make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
@@ -586,22 +615,23 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
                     if (ok) publish();
                 }
-                ok = ok && warp_wait(&bars[FULL + (cc & 1)], (cc >> 1) & 1, stop);
-                if (ok) split(0, cc & 1);
+                ok = ok && warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
+                if (ok) split(0, ring);
             }
-            for (int c = 0; ok && c < nc; ++c, ++cc) {
+            for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
                 if (!(ok = warp_wait(&bars[DSFULL], cc & 1, stop))) break;
                 // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
                 // here, so that its product runs while S is updated
                 const bool more = c + 1 < nc;
-                const uint32_t s1 = (cc + 1) & 1, par1 = ((cc + 1) >> 1) & 1;
-                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + s1], par1));
+                Ring then = ring;
+                then.step();
+                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + then.s], then.phase()));
 #pragma unroll 1
                 for (int step = 0; ok && step < 2; ++step) {
                     if ((step == 0) == ahead) {
                         if (!more) continue;
-                        ok = warp_wait(&bars[FULL + s1], par1, stop);
-                        if (ok) split(c + 1, s1);
+                        ok = warp_wait(&bars[FULL + then.s], then.phase(), stop);
+                        if (ok) split(c + 1, then);
                         continue;
                     }
                     tc_fence_after();
