@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
                            : it.l < 0.f ? (int)fminf(6.f / (C * -it.l) + 2.f, 1e9f)
                                         : 1 << 30;
-                // the next block is taken only when this item's last loads are due, so that none waits here while
-                // another SM is idle
+                // the next block is taken only when this item's last three loads are due: early enough to be announced
+                // by then, late enough that none waits here while another SM is idle
                 bool ok = !g.ok || (announce(it) && mbar_wait(&bars[LASTLOAD], (put - 1) & 1, stop, kItemWait));
                 if (ok) {
                     mbar_arrive_expect_tx(&bars[NEXT], 16);
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         ok = ok && freed(KFREE, i) && (!kOut || freed(QFREE, i)) && freed(VFREE, i);
                 if (nc == 0) mbar_arrive(&bars[LASTLOAD]);
                 for (int c = 0; ok && c < nc; ++c) {
-                    if (c == nc - 1) mbar_arrive(&bars[LASTLOAD]);
+                    if (c == max(0, nc - 3)) mbar_arrive(&bars[LASTLOAD]);
                     const int s = ring.s, r = row0 + place_of(rev, nc, c) * C;
                     ok = freed(KFREE, s);
                     mbar_arrive_expect_tx(&bars[FULL + s], (ring.kb + 1 + (kOut ? ring.kb : 0)) * kBox);
@@ -611,12 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 warp_arrive(&bars[VREADY], lane);
             };
             if (nc > 0) {
-                if (kOut) {  // over the S that the item before left, once it has been read
+                ok = warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
+                if (ok) split(0, ring);  // while the loads of S are under way
+                if (ok && kOut) {  // over the S that the item before left, once it has been read
                     ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
                     if (ok) publish();
                 }
-                ok = ok && warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
-                if (ok) split(0, ring);
             }
             for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
                 if (!(ok = warp_wait(&bars[DSFULL], cc & 1, stop))) break;
