@@ -91,6 +91,7 @@ struct Item {
     int slot, seq;
     int row0, nc, last;  // first row, chunks, rows of the chunk that ends the sequence (or segment)
     int third;           // the last chunks, in scan order, whose V' needs its third part
+    int rev;
     float l;
 };
 static_assert(sizeof(Item) * kItems <= 512 - 288, "the ring's place");
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 it.nc = (int)((g.n + C - 1) / C);
                 it.last = (int)(g.n - (int64_t)(it.nc - 1) * C);
                 it.l = a.log_decay[it.h];
+                it.rev = a.reverse;
                 // What the second part leaves (2^-16) shows in a state that the caller gets unless at least d rows follow
                 // with e^{l d} < 2^-8: l d < -6.
                 it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
@@ -548,33 +550,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             fence_async_smem();
             warp_arrive(&bars[SREADY], lane);
         };
+        // the item is read from its place in the ring wherever it is needed, not kept in registers
         for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
-            const ScanArgs& a = prm.scan[it->scan].a;
-            const int nc = it->nc, last = it->last, third = it->third;
-            const float l = it->l;
-            const bool rev = a.reverse;
-            ring.cut(a.Dk, kOut);
-            const int d0 = it->dv0 + half * kHalf;
-            // the state's place among the sequences' or the segments'
-            const int state = (kMode == kWhole ? it->seq : it->slot) * a.H + it->h;
-            leave(k, true);
-            {
-                const float* init = kMode == kOutputs ? a.seg_state : kMode == kStates ? nullptr : a.init;
-                const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
-                const float* p = init + (size_t)state * a.Dk * a.Dv + (init_t ? (size_t)d0 * a.Dk + row : (size_t)row * a.Dv + d0);
-                const int step = init_t ? a.Dk : 1;
-#pragma unroll
-                for (int d = 0; d < kHalf; ++d) S[d] = init && row < a.Dk && d0 + d < a.Dv ? p[d * step] : 0.f;
-            }
-            auto weight = [&](int n) {  // of tile row `row` in the state behind a chunk of n rows
-                return a.w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row);
+            ring.cut(prm.scan[it->scan].a.Dk, kOut);
+            auto rows = [&](int c) { return rows_of(place_of(it->rev, it->nc, c), it->nc, it->last); };
+            // weight of tile row `row` in the state behind a chunk of n rows
+            auto weight = [&](int n) {
+                return row < n ? prm.scan[it->scan].a.w_scale * decay_pow(it->l, it->rev ? row + 1 : n - 1 - row) : 0.f;
             };
-            const float w_full = weight(C), decay_full = decay_pow(l, C);
+            const float w_full = weight(C), decay_full = decay_pow(it->l, C);
             auto split = [&](int c, const Ring& at) {  // V' of chunk c; zeros behind the sequence's end
-                const int n = rows_of(place_of(rev, nc, c), nc, last);
-                const bool three = kMaxParts == 3 && nc - c <= third;
+                const int n = rows(c);
+                const bool three = kMaxParts == 3 && it->nc - c <= it->third;
                 uint8_t* tv = sm + at.v(kOut);
-                const float wr = n == C ? w_full : row < n ? weight(n) : 0.f;
+                const float wr = n == C ? w_full : weight(n);
                 if (row >= n) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -584,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (i / 4 == half) *reinterpret_cast<uint4*>(tv + o) = z;
                     }
                 }
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < kHalf / 8; ++i) {
                     const uint32_t o = sw128_off(row, half * 4 + i);
                     const uint4 x = *reinterpret_cast<const uint4*>(tv + o);
@@ -610,19 +599,49 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 fence_async_smem();
                 warp_arrive(&bars[VREADY], lane);
             };
-            if (nc > 0) {
+            // this row of the state, where it is kept: among the sequences' or the segments'
+            auto state_row = [&](const float* base, bool transposed) {
+                const ScanArgs& a = prm.scan[it->scan].a;
+                const int d0 = it->dv0 + half * kHalf;
+                return base + (size_t)((kMode == kWhole ? it->seq : it->slot) * a.H + it->h) * a.Dk * a.Dv +
+                       (transposed ? (size_t)d0 * a.Dk + row : (size_t)row * a.Dv + d0);
+            };
+            const int live = prm.scan[it->scan].a.Dv - (it->dv0 + half * kHalf);  // channels of this half
+            if (it->nc > 0) {
                 ok = warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
-                if (ok) split(0, ring);  // while the loads of S are under way
-                if (ok && kOut) {  // over the S that the item before left, once it has been read
+                if (ok) split(0, ring);
+            }
+#pragma unroll
+            for (int d = 0; d < kHalf; ++d) S[d] = 0.f;
+            if (kMode != kStates) {
+                const ScanArgs& a = prm.scan[it->scan].a;
+                const float* init = kMode == kOutputs ? a.seg_state : a.init;
+                const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
+                if (init && row < a.Dk) {
+                    const float* src = state_row(init, init_t);
+                    if (init_t) {  // neighbouring lanes' values lie side by side
+#pragma unroll
+                        for (int d = 0; d < kHalf; ++d)
+                            if (d < live) S[d] = src[d * a.Dk];
+                    } else {  // a row per lane: the memory pipe takes a pass for each lane, so as few accesses as can be
+#pragma unroll
+                        for (int d = 0; d < kHalf; d += 4)
+                            if (d < live) {
+                                const float4 x = *reinterpret_cast<const float4*>(src + d);
+                                S[d] = x.x; S[d + 1] = x.y; S[d + 2] = x.z; S[d + 3] = x.w;
+                            }
+                    }
+                }
+                if (ok && it->nc > 0) {  // over the S that the item before left, once it has been read
                     ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
                     if (ok) publish();
                 }
             }
-            for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
+            for (int c = 0; ok && c < it->nc; ++c, ++cc, ring.step()) {
                 if (!(ok = warp_wait(&bars[DSFULL], cc & 1, stop))) break;
                 // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
                 // here, so that its product runs while S is updated
-                const bool more = c + 1 < nc;
+                const bool more = c + 1 < it->nc;
                 Ring then = ring;
                 then.step();
                 const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + then.s], then.phase()));
@@ -635,21 +654,21 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         continue;
                     }
                     tc_fence_after();
-                    const int n = rows_of(place_of(rev, nc, c), nc, last);
-                    const float e = n == C ? decay_full : decay_pow(l, n);
+                    const int n = rows(c);
+                    const float e = n == C ? decay_full : decay_pow(it->l, n);
 #pragma unroll
-                    for (int b = 0; b < kHalf / 16; ++b) {
-                        const uint32_t col = lane_base + COL_DS + (cc & 1) * 128 + half * kHalf + b * 16;
-                        float x[16], y[16];
-                        tmem_ld16(col, x);
-                        tmem_ld16(col + 64, y);
+                    for (int b = 0; b < kHalf / 8; ++b) {  // 8 at a time: this is where the role's registers run out
+                        const uint32_t col = lane_base + COL_DS + (cc & 1) * 128 + half * kHalf + b * 8;
+                        float x[8], y[8];
+                        tmem_ld8(col, x);
+                        tmem_ld8(col + 64, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
+                        for (int j = 0; j < 8; j += 2) {
                             const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
-                            const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 16 + j], S[b * 16 + j + 1]), d);
-                            S[b * 16 + j] = f.x;
-                            S[b * 16 + j + 1] = f.y;
+                            const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 8 + j], S[b * 8 + j + 1]), d);
+                            S[b * 8 + j] = f.x;
+                            S[b * 8 + j + 1] = f.y;
                         }
                     }
                     tc_fence_before();
@@ -659,13 +678,17 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     }
                 }
             }
-            float* fin = kMode == kOutputs ? nullptr : kMode == kStates ? a.seg_state : a.final_state;
-            if (ok && fin && row < a.Dk) {
-                float* p = fin + (size_t)state * a.Dk * a.Dv + (size_t)row * a.Dv + d0;
+            if (kMode != kOutputs) {
+                const ScanArgs& a = prm.scan[it->scan].a;
+                float* fin = kMode == kStates ? a.seg_state : a.final_state;
+                if (ok && fin && row < a.Dk) {
+                    float* dst = const_cast<float*>(state_row(fin, false));
 #pragma unroll
-                for (int d = 0; d < kHalf; d += 4)
-                    if (d0 + d < a.Dv) *reinterpret_cast<float4*>(p + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
+                    for (int d = 0; d < kHalf; d += 4)
+                        if (d < live) *reinterpret_cast<float4*>(dst + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
+                }
             }
+            leave(k, true);
         }
         if (!ok) *stop = 1;
     } else {
