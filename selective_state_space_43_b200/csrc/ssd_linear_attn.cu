@@ -228,38 +228,49 @@ cudaError_t launch_scans(const ScanArgs* scans, int count, Mode mode, cudaStream
 // ---- cutting the sequence axis ------------------------------------------------------------------------------
 // A scan walks its rows one chunk behind the other, so a call with few (sequence, head) pairs leaves SMs
 // idle.  Cut into segments it takes two passes (the state each segment leaves, joined, then the outputs from
-// the joined states), which read keys and values twice.  The choice compares modelled times in microseconds:
-// a block costs kStart, and per row kRow for outputs (and states) or kStateRow for states alone; blocks run
-// kSlots at a time; the cut adds two launches (kExtra) and the writing, joining and reading of its states.
-// Measured on B200 with bf16 rows, 8192 rows of 16 heads, 128 x 128: see the figures beside each.
+// the joined states), which read keys and values twice.  The choice compares modelled times in microseconds: a block
+// costs `start`, and per row `row` for outputs and state or `state_row` for states alone; blocks run `slots` at a
+// time in each of a pass's launches; the cut adds two launches (`extra`) and the writing, joining and reading of its
+// states at `state_rate` bytes a microsecond.  Both sides of the rule as measured (B200, whole sequences against the
+// chosen cut): bf16, 1 x 8191 rows, 16 heads of 128 x 128: 143 against 89 us (2048 rows; 126 to 140 us at 1024 and
+// 4096); 4 x 8192 rows, 64 heads of 128 x 64: 324 us whole (579 at 4096 rows).  fp32, 1 x 256 rows, 4 heads of 32 x 64:
+// 42 against 17 us (32 rows); 2 x 2048 rows, 8 heads of 128 x 128: 760 against 193 us (256 rows); 16 x 300 rows, 8
+// heads of 96 x 64: 103 us whole (126 at 128 rows).
 struct Cost {
-    double start, row, state_row, extra, slots;
+    double start, row, state_row, extra, state_rate, slots;
+    int64_t least;  // rows of a segment: a chunk of the kernel
+    bool together;  // a pass's scans are one launch
 };
 Cost cost_of(bool bf16, int Dk) {
-    // tensor cores, one block per SM: 2.0 us a 128-row chunk, 1.2 us of it for states alone;
-    // CUDA cores, two blocks per SM at Dk = 128
-    return bf16 ? Cost{5.0, 2.0 / 128, 1.2 / 128, 6.0, 148.0}
-                : Cost{5.0, 0.6 * Dk / 128, 0.25 * Dk / 128, 6.0, Dk > 64 ? 296.0 : 592.0};
+    if (bf16) return Cost{5.0, 2.0 / 128, 1.2 / 128, 6.0, 5e6, 148.0, 256, true};
+    const double row = 0.06 + 0.0024 * Dk;
+    return Cost{5.0, row, 0.45 * row, 10.0, 2.5e6, Dk > 64 ? 220.0 : 450.0, 32, false};
 }
-// Rows of a segment (a multiple of 128), or 0: whole sequences.  `blocks`: blocks of the output pass for each
-// sequence; `state_blocks`: of the states' pass.
+// Rows of a segment, or 0: whole sequences.  `blocks`: blocks of the output pass for each sequence, of `scans` scans;
+// `state_blocks`, `state_scans`: of the states' pass.
 int64_t segment_rows(int64_t batch, int64_t L, int64_t rows, bool packed, bool bf16, int Dk, int Dv, int64_t H,
-                     int64_t blocks, int64_t state_blocks) {
+                     int64_t blocks, int scans, int64_t state_blocks, int state_scans) {
     if (batch == 0 || rows == 0) return 0;
     const Cost k = cost_of(bf16, Dk);
     const double mean = (double)rows / batch;
     // the longest of a packed batch is not known here; three times the mean is usual for prompts
     const double longest = packed ? fmin((double)rows, 3.0 * mean) : (double)L;
-    auto waves = [&](double n) { return n <= k.slots ? 1.0 : packed ? n / k.slots + 0.5 : ceil(n / k.slots); };
-    const double all = (double)batch * blocks;
-    double best = fmax(waves(all) * (k.start + mean * k.row), k.start + longest * k.row);
+    auto waves = [&](double n, int launches) {
+        if (k.together) launches = 1;
+        const double w = n / launches / k.slots;
+        return launches * (w <= 1.0 ? 1.0 : bf16 && !packed ? ceil(w) : w);
+    };
+    const int launches = k.together ? 1 : scans;
+    double best = fmax(waves((double)batch * blocks, scans) * (k.start + mean * k.row), launches * (k.start + longest * k.row));
     int64_t seg = 0;
-    for (int64_t m = 256; m < longest; m *= 2) {
+    int64_t m = k.least;
+    while (m * 2 < longest) m *= 2;
+    for (; m >= k.least && m < longest; m /= 2) {  // the longest that is not 10 % worse than a shorter one
         const double slots = packed ? rows / (double)m + 0.5 * batch : batch * ceil((double)L / m);
-        const double bytes = slots * H * Dk * Dv * 4 * 4;  // written, read and written, read
+        const double bytes = slots * H * Dk * Dv * 4 * 4 * state_scans;  // written, read and written, read
         const double part = fmin((double)m, mean);
-        const double t = waves(slots * state_blocks) * (k.start + part * k.state_row) +
-                         waves(slots * blocks) * (k.start + part * k.row) + k.extra + bytes / 5e6;
+        const double t = waves(slots * state_blocks, state_scans) * (k.start + part * k.state_row) +
+                         waves(slots * blocks, scans) * (k.start + part * k.row) + k.extra + bytes / k.state_rate;
         if (t < 0.9 * best) {
             best = t;
             seg = m;
@@ -271,11 +282,12 @@ int64_t value_blocks(int64_t H, int Dv) { return H * ((Dv + 63) / 64); }
 
 int64_t prefill_segment(const ssd_linear_attn_dims* d, bool bf16, bool packed, int64_t rows) {
     const int64_t b = value_blocks(d->nheads, d->value_dim);
-    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, b, b);
+    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, b, 1, b, 1);
 }
 int64_t backward_segment(const ssd_linear_attn_dims* d, bool bf16, bool packed, int64_t rows) {
     const int64_t k = value_blocks(d->nheads, d->key_dim), v = value_blocks(d->nheads, d->value_dim);
-    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, 2 * k + v, k + v);
+    return segment_rows(d->batch, d->seqlen, rows, packed, bf16, d->key_dim, d->value_dim, d->nheads, 2 * k + v, 3,
+                        k + v, 2);
 }
 // Bytes of one scan's segment states.
 size_t segment_bytes(const ssd_linear_attn_dims* d, bool packed, int64_t rows, int64_t seg) {
