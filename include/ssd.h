@@ -449,7 +449,8 @@ SSD_API ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* dims, ssd
  * Gradients of the chunked form: of sum(d_o * o) + sum(d_final_state * final_state).
  * q, k, v, d_o contiguous; dq, dk, dv (out) laid out as q, k, v in dtype (shared key
  * and value heads: the sum over their query heads, taken in fp32).  init_state and d_final_state may be
- * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.
+ * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.  A non-finite value reaches the
+ * gradients of its own sequence and head only.
  */
 SSD_API size_t ssd_linear_attn_backward_workspace_bytes(const ssd_linear_attn_dims* dims, ssd_dtype dtype, int packed);
 SSD_API ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* dims, ssd_dtype dtype, const float* log_decay,

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace ssd {
 
 // Activation / output types: fp32 in and out; bf16 in and out; bf16 in, fp32 y.
@@ -67,6 +69,19 @@ __device__ inline SeqSpan seq_span(const PrefillArgs& a, int64_t b) {
     const int64_t r0 = a.cu[b], r1 = a.cu[b + 1];
     if (r0 < 0 || r1 < r0 || r1 > a.L) return SeqSpan{0, 0, false};
     return SeqSpan{r0, r1 - r0, true};
+}
+
+// Allows `kernel` that much dynamic shared memory on the current device (once for each device).
+template <auto kernel> cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // The device error word of the current device (nullptr if it cannot be found).

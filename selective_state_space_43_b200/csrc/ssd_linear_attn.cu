@@ -186,7 +186,7 @@ ssd_status check_dims(const ssd_linear_attn_dims* d, ssd_dtype dtype) {
     if (d->nheads <= 0 || d->kv_heads <= 0 || d->nheads % d->kv_heads != 0 || d->nheads > 65535) return SSD_ERR_SHAPE;
     for (int w : {d->key_dim, d->value_dim})
         if (w < 8 || w > 128 || w % 8 != 0) return SSD_ERR_SHAPE;
-    if (d->batch > (1LL << 31) - 1 || d->batch * (int64_t)d->nheads > (1LL << 30) - 1) return SSD_ERR_SHAPE;
+    if (d->batch > (1LL << 31) - 1 || d->batch * (int64_t)d->nheads > (1LL << 28)) return SSD_ERR_SHAPE;
     return SSD_OK;
 }
 

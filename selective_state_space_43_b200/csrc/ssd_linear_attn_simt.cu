@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
 
 template <int DKP, int MODE>
 cudaError_t launch(const ScanArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(scan_simt_kernel<DKP, MODE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<DKP>());
+    const cudaError_t e = allow_smem<scan_simt_kernel<DKP, MODE>>((int)smem_bytes<DKP>());
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.seg_len ? a.slots : a.batch), a.H, (a.Dv + DVB - 1) / DVB);
     scan_simt_kernel<DKP, MODE><<<grid, kThreads, smem_bytes<DKP>(), st>>>(a);

@@ -12,14 +12,14 @@
 // Because the decay is a constant of the head, D, w and the output coefficients are the same for every chunk:
 // each thread computes its 64 mask entries, its row weight and its coefficient once and keeps them in
 // registers, so a score costs one multiply and half a conversion.  The state S is held in fp32 in the
-// registers of one warpgroup (32 channels of a key row per thread), dS is computed from zero each chunk: no
-// accumulator is carried through the tensor cores, and nothing but that warpgroup's multiply-adds depends on the
+// registers of two warpgroups (32 channels of a key row per thread), dS is computed from zero each chunk: no
+// accumulator is carried through the tensor cores, and nothing but those warps' multiply-adds depends on the
 // chunk before.
 //
-// Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself
-// stays fp32); o once.  V' is cut into bf16 parts of 8 bits
-// (v w = hi + mid + lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits) where what the second leaves
-// would show in a state that the caller gets, so that such a state is as exact as fp32 sums.
+// Roundings: scores (times their decay) to bf16, the A operand of Y1 (in a sequence of one chunk to two bf16 parts); the
+// copy of S that Y2 reads to bf16 (S itself stays fp32); o once.  V' is cut into bf16 parts of 8 bits (v w = hi + mid +
+// lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits) where what the second leaves would show in a
+// state that the caller gets, so that such a state is as exact as fp32 sums.
 //
 // 24 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
@@ -56,7 +56,7 @@ constexpr int kStages = 3;  // at most
 enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, PFULL = 12, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE,
            NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
 static_assert(kBars * 8 <= 240, "the barriers' place");
-// TMEM columns: scores (their bf16 form overlays each half), Y1, Y2, dS (two buffers of two parts)
+// TMEM columns: scores (their bf16 form takes the place of each 16), Y1, Y2, dS (two buffers of two parts)
 constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
 
 // Up to three scans in one launch (a gradient's), their blocks one behind the other.
@@ -276,6 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (whole_warp) __syncwarp();
         if (!whole_warp || lane == 0) mbar_arrive(&bars[IEMPTY + number % kItems]);
     };
+    // Whether the scores are kept in two bf16 parts: a lone chunk may have few outputs, which all share a score's error.
+    auto two_parts = [](int nc) { return nc == 1; };
     // the place of chunk c, in scan order, among the item's chunks; the rows of the chunk at a place
     auto place_of = [](bool rev, int nc, int c) { return rev ? nc - 1 - c : c; };
     auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };
@@ -444,9 +446,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         const uint64_t dV = sw128_desc(tv, 16384, 1024);
                         if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)  // the bf16 scores: 64 to the first 32 columns of each half
-                                mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + (k >> 2) * 64 + (k & 3) * 8, dV + k * 128, ID_Y,
-                                            k > 0);
+                            for (int k = 0; k < 8; ++k)  // the bf16 scores: 16 to the first 8 of every 16 columns
+                                mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + k * 16, dV + k * 128, ID_Y, k > 0);
+                            if (two_parts(nc)) {  // and what they leave, in the other 8
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + k * 16 + 8, dV + k * 128, ID_Y, 1);
+                            }
                             mma_commit(&bars[YFULL]);
                         }
                         __syncwarp();
@@ -518,9 +524,17 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             for (int j = 0; j < 8; ++j) {
                                 const float2 f = __fmul2_rn(make_float2(v[i][2 * j], v[i][2 * j + 1]),
                                                             make_float2(m[j1 + 2 * j], m[j1 + 2 * j + 1]));
+                                v[i][2 * j] = f.x;
+                                v[i][2 * j + 1] = f.y;
                                 p[j] = pack_bf2(f.x, f.y);
                             }
-                            tmem_st8(col + (b + i) * 8, p);  // over columns already read
+                            tmem_st8(col + j1, p);  // over the columns just read
+                            if (two_parts(nc)) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    p[j] = pack_bf2(v[i][2 * j] - bf_lo(p[j]), v[i][2 * j + 1] - bf_hi(p[j]));
+                                tmem_st8(col + j1 + 8, p);
+                            }
                         }
                     }
                     tmem_wait_st();
@@ -783,8 +797,7 @@ bool make_map(CUtensorMap* m, const void* base, int width, int heads, int64_t ro
 }
 
 template <int kMode> cudaError_t launch(const Params& prm, unsigned blocks, cudaStream_t st) {
-    static const cudaError_t e = cudaFuncSetAttribute(scan_tc_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      (int)kSmemBytes);
+    const cudaError_t e = allow_smem<scan_tc_kernel<kMode>>((int)kSmemBytes);
     if (e != cudaSuccess) return e;
     scan_tc_kernel<kMode><<<blocks, kThreads, kSmemBytes, st>>>(prm);
     return cudaGetLastError();
@@ -794,21 +807,22 @@ template <int kMode> cudaError_t launch(const Params& prm, unsigned blocks, cuda
 
 cudaError_t launch_scan_tc(const ScanArgs* scans, int count, Mode mode, cudaStream_t st) {
     Params prm;
-    unsigned blocks = 0;
+    int64_t blocks = 0;
     for (int i = 0; i < count; ++i) {
         const ScanArgs& a = scans[i];
         Scan& s = prm.scan[i];
         s.a = a;
-        s.blocks = (unsigned)((a.seg_len ? a.slots : a.batch) * a.H * ((a.Dv + DVB - 1) / DVB));
-        blocks += s.blocks;
+        const int64_t n = (a.seg_len ? a.slots : a.batch) * a.H * ((a.Dv + DVB - 1) / DVB);
+        if ((blocks += n) > 0x7fffffff) return cudaErrorInvalidValue;
+        s.blocks = (unsigned)n;
         if (a.rows > 0 && (!make_map(&s.tk, a.k, a.Dk, a.H / a.gk, a.rows, a.rs_k) ||
                            !make_map(&s.tv, a.v, a.Dv, a.H / a.gv, a.rows, a.rs_v) ||
                            (mode != kStates && !make_map(&s.tq, a.q, a.Dk, a.H / a.gq, a.rows, a.rs_q))))
             return cudaErrorInvalidValue;
     }
     if (blocks == 0) return cudaSuccess;
-    if (mode == kStates) return launch<kStates>(prm, blocks, st);
-    return mode == kOutputs ? launch<kOutputs>(prm, blocks, st) : launch<kWhole>(prm, blocks, st);
+    if (mode == kStates) return launch<kStates>(prm, (unsigned)blocks, st);
+    return mode == kOutputs ? launch<kOutputs>(prm, (unsigned)blocks, st) : launch<kWhole>(prm, (unsigned)blocks, st);
 }
 
 }  // namespace la

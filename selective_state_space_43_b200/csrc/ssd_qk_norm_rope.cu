@@ -17,6 +17,7 @@
 
 #include "ssd.h"
 #include "ssd_common.cuh"
+#include "ssd_internal.h"
 
 namespace ssd {
 namespace rope {
@@ -347,8 +348,7 @@ int tokens_per_block(int64_t tokens, int heads) {
 template <typename T, int kRun, int LPR, bool kInter, bool kBackward>
 cudaError_t launch_one(const Args& a, unsigned blocks, cudaStream_t st) {
     constexpr int bytes = smem_bytes<T, kRun, kBackward>();
-    static const cudaError_t e = cudaFuncSetAttribute(qk_norm_rope_kernel<T, kRun, LPR, kInter, kBackward>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem<qk_norm_rope_kernel<T, kRun, LPR, kInter, kBackward>>(bytes);
     if (e != cudaSuccess) return e;
     qk_norm_rope_kernel<T, kRun, LPR, kInter, kBackward><<<dim3(blocks, 2), kThreads, bytes, st>>>(a);
     return cudaGetLastError();

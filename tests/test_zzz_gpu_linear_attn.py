@@ -417,3 +417,13 @@ def test_bad_offsets_in_segments(dtype):
         with pytest.raises(ops.SsdError):
             ops.device_status()
         ops.device_status()
+
+
+@pytest.mark.parametrize("L,H,dk,dv", [(1, 1, 64, 64), (1, 3, 128, 8), (2, 1, 32, 128), (5, 2, 64, 64), (128, 1, 96, 96)])
+def test_a_lone_chunk_rounds_its_outputs_only(L, H, dk, dv):
+    """Few outputs may share one score, whose rounding would then be all of theirs: a sequence of one chunk keeps its
+    scores in two bf16 parts (2^-16 of themselves off), so that only the outputs' own rounding shows."""
+    x = make(L + dk, (3, L), H, H, dk, dv, torch.bfloat16)
+    o, _ = ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"])
+    wo, _, mo, _ = lo.prefill(x["q"], x["k"], x["v"], x["log_decay"], dk ** -0.5)
+    assert (np.abs(np64(o) - wo) <= U * np.abs(wo) * 1.001 + (2.0 ** -15 + n_terms(L, dk) * E) * mo).all()
