@@ -108,35 +108,45 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Co
     const int64_t nseg = (s.len + a.seg_len - 1) / a.seg_len, slot0 = first_slot(a, b, s);
     const float whole = decay_pow(l, a.seg_len);
     const float last = decay_pow(l, s.len - (nseg - 1) * a.seg_len);
-#pragma unroll 4
-    for (int64_t j = 0; j < nseg; ++j) {
-        const int64_t i = a.reverse ? nseg - 1 - j : j;
-        float* p = a.seg_state + ((size_t)(slot0 + i) * a.H + h) * size + e;
-        const float4 x = load4(p);
-        const float d = i == nseg - 1 ? last : whole;
-        store4(p, R);
-        R.x = fmaf(d, R.x, x.x);
-        R.y = fmaf(d, R.y, x.y);
-        R.z = fmaf(d, R.z, x.z);
-        R.w = fmaf(d, R.w, x.w);
+    // eight segments' states are loaded before the first is overwritten: one after the other would be a chain of latencies
+    float* first = a.seg_state + (size_t)h * size + e;
+    const int64_t pitch = (int64_t)a.H * size;
+    for (int64_t j0 = 0; j0 < nseg; j0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < nseg) x[j] = load4(first + (slot0 + (a.reverse ? nseg - 1 - j0 - j : j0 + j)) * pitch);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j < nseg) {
+                const int64_t i = a.reverse ? nseg - 1 - j0 - j : j0 + j;
+                const float d = i == nseg - 1 ? last : whole;
+                store4(first + (slot0 + i) * pitch, R);
+                R.x = fmaf(d, R.x, x[j].x);
+                R.y = fmaf(d, R.y, x[j].y);
+                R.z = fmaf(d, R.z, x[j].z);
+                R.w = fmaf(d, R.w, x[j].w);
+            }
+        }
     }
     if (a.final_state) store4(a.final_state + ((size_t)b * a.H + h) * size + e, R);
 }
 
 // ---- gradients of shared heads ------------------------------------------------------------------------------
-template <typename T>
-__global__ void __launch_bounds__(256) group_sum_kernel(const float* src, T* dst, int64_t quads, int group, int width) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= quads) return;
-    const int per = width / 4;
+template <typename T> __global__ void __launch_bounds__(256) group_sum_kernel(GroupSums a) {
+    const int which = blockIdx.x >= a.sum[0].blocks;
+    const GroupSum& g = a.sum[which];
+    const int64_t i = (int64_t)(blockIdx.x - (which ? a.sum[0].blocks : 0)) * 256 + threadIdx.x;
+    if (i >= g.quads) return;
+    const int per = g.width / 4;
     const int64_t head = i / per;  // (row, head) of dst
-    const float* p = src + (head * group * per + (i - head * per)) * 4;
+    const float* p = g.src + (head * a.group * per + (i - head * per)) * 4;
     float4 t = load4(p);
-    for (int g = 1; g < group; ++g) {
-        const float4 u = load4(p + (size_t)g * width);
+    for (int k = 1; k < a.group; ++k) {
+        const float4 u = load4(p + (size_t)k * g.width);
         t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
     }
-    store4(dst + i * 4, t);
+    store4(static_cast<T*>(g.dst) + i * 4, t);
 }
 
 }  // namespace
@@ -157,16 +167,19 @@ cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_group_sum(const float* src, void* dst, int64_t rows, int heads, int group, int width, bool bf16,
-                             cudaStream_t st) {
-    const int64_t quads = rows * heads * (width / 4);
-    if (quads == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)((quads + 255) / 256);
+cudaError_t launch_group_sums(GroupSums a, int64_t rows, int heads, bool bf16, cudaStream_t st) {
+    int64_t blocks = 0;
+    for (GroupSum& g : a.sum) {
+        g.quads = rows * heads * (g.width / 4);
+        g.blocks = (unsigned)((g.quads + 255) / 256);
+        blocks += g.blocks;
+    }
+    if (blocks == 0) return cudaSuccess;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     if (bf16)
-        group_sum_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(src, static_cast<__nv_bfloat16*>(dst), quads, group,
-                                                                 width);
+        group_sum_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(a);
     else
-        group_sum_kernel<float><<<blocks, 256, 0, st>>>(src, static_cast<float*>(dst), quads, group, width);
+        group_sum_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -483,8 +496,8 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dty
     } else {
         e = launch_scans(a, 3, kWhole, cs);
     }
-    if (e == cudaSuccess && group > 1) e = launch_group_sum(dk_heads, dk, rows, (int)Hk, group, (int)Dk, base.bf16, cs);
-    if (e == cudaSuccess && group > 1) e = launch_group_sum(dv_heads, dv, rows, (int)Hk, group, (int)Dv, base.bf16, cs);
+    if (e == cudaSuccess && group > 1)
+        e = launch_group_sums(GroupSums{{{dk_heads, dk, (int)Dk}, {dv_heads, dv, (int)Dv}}, group}, rows, (int)Hk, base.bf16, cs);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

@@ -108,9 +108,20 @@ cudaError_t launch_scan_tc(const ScanArgs* scans, int count, Mode mode, cudaStre
 // order, from init), final_state the state behind the last one.
 // One or two scans of a call in one launch.
 cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st);
-// dst[row][head][:] = sum over the `group` scan heads that share the head of src[row][head * group + g][:].
-cudaError_t launch_group_sum(const float* src, void* dst, int64_t rows, int heads, int group, int width, bool bf16,
-                             cudaStream_t st);
+// dst[row][head][:] = sum over the `group` scan heads that share the head of src[row][head * group + g][:]; two
+// such sums (of keys and of values) in one launch.
+struct GroupSum {
+    const float* src;
+    void* dst;
+    int width;
+    int64_t quads;    // set by the launch
+    unsigned blocks;
+};
+struct GroupSums {
+    GroupSum sum[2];
+    int group;
+};
+cudaError_t launch_group_sums(GroupSums a, int64_t rows, int heads, bool bf16, cudaStream_t st);
 
 struct DecodeArgs {
     int64_t batch;
