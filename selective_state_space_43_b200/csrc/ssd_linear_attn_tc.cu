@@ -50,7 +50,9 @@ constexpr uint32_t OFF_VP = 10 * kBox;           // behind the stages; V': up to
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
 constexpr uint32_t OFF_STOP = OFF_BAR + 240, OFF_TMEM = OFF_BAR + 248, OFF_ANSWER = OFF_BAR + 256, OFF_ITEM = OFF_BAR + 288;
-constexpr uint32_t kSmemBytes = OFF_BAR + 512 + 1024;  // + alignment of the base
+constexpr uint32_t OFF_ORDER = OFF_BAR + 512;
+constexpr int kSorted = 64;   // packed sequences that are taken longest first
+constexpr uint32_t kSmemBytes = OFF_ORDER + kSorted + 1024;  // + alignment of the base
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
 constexpr int kStages = 3;  // at most
 enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, PFULL = 12, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE,
@@ -284,58 +286,80 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
 
     if (warp >= kWarpTma) {
         regs_fewer<48>();
-        if (warp == kWarpItem && lane == 0) {
+        if (warp == kWarpItem) {
             // ---- items ----
-            int64_t block = blockIdx.x;
-            int put = 0;
-            auto announce = [&](const Item& it) {
-                const int i = put % kItems;
-                if (put >= kItems && !mbar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
-                items[i] = it;
-                mbar_arrive(&bars[IFULL + i]);
-                ++put;
-                return true;
-            };
-            for (int asked = 0;; ++asked) {
-                Item it;
-                it.scan = 0;
-                unsigned b = (unsigned)block;
-                while (b >= prm.scan[it.scan].blocks) b -= prm.scan[it.scan++].blocks;
-                const ScanArgs& a = prm.scan[it.scan].a;
-                const unsigned ndvb = (a.Dv + DVB - 1) / DVB;
-                it.dv0 = (int)(b % ndvb) * DVB;
-                it.h = (int)(b / ndvb % a.H);
-                it.slot = (int)(b / (ndvb * (unsigned)a.H));
-                const Segment g = segment_of(a, it.slot);
-                if (a.cu && a.seg_len == 0 && it.h == 0 && it.dv0 == 0 && !sequence_span(a, it.slot).ok)
-                    atomicOr(a.err, kErrBadSeqlens);
-                it.seq = (int)g.seq;
-                it.row0 = (int)g.row0;
-                it.nc = (int)((g.n + C - 1) / C);
-                it.last = (int)(g.n - (int64_t)(it.nc - 1) * C);
-                it.l = a.log_decay[it.h];
-                it.rev = a.reverse;
-                // What the second part leaves (2^-16) shows in a state that the caller gets unless at least d rows follow
-                // with e^{l d} < 2^-8: l d < -6.
-                it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
-                           : it.l < 0.f ? (int)fminf(6.f / (C * -it.l) + 2.f, 1e9f)
-                                        : 1 << 30;
-                // the next block is taken only when this item's last three loads are due: early enough to be announced
-                // by then, late enough that none waits here while another SM is idle
-                bool ok = !g.ok || (announce(it) && mbar_wait(&bars[LASTLOAD], (put - 1) & 1, stop, kItemWait));
-                if (ok) {
-                    mbar_arrive_expect_tx(&bars[NEXT], 16);
-                    ask_next_block(answer, &bars[NEXT]);
-                    ok = mbar_wait(&bars[NEXT], asked & 1, nullptr);
-                    block = next_block(answer);
-                    fence_async_smem();  // read before the next answer is written
+            const ScanArgs& call = prm.scan[0].a;  // a launch's scans have the same sequences
+            const bool sorted = call.cu && call.seg_len == 0 && call.batch <= kSorted && gridDim.x > 148;
+            uint8_t* order = sm + OFF_ORDER;
+            if (sorted) {
+                // Packed sequences are taken longest first, so that no long one starts when the other SMs run out of work
+                // (24 ragged prompts of 16384 rows in all, 40 heads: 137 -> 122 us); more of them even out by themselves:
+                // sequence i goes to the place that the number of longer ones (and equal ones before it) gives.
+                const int n = (int)call.batch;
+                for (int i = lane; i < n; i += 32) {
+                    const int len = (int)sequence_span(call, i).len;
+                    int rank = 0;
+                    for (int j = 0; j < n; ++j) {
+                        const int other = (int)sequence_span(call, j).len;
+                        rank += other > len || (other == len && j < i);
+                    }
+                    order[rank] = (uint8_t)i;
                 }
-                if (!ok) *stop = 1;
-                if (!ok || block < 0) break;
+                __syncwarp();
             }
-            Item end;
-            end.scan = -1;
-            if (!announce(end)) *stop = 1;
+            if (lane == 0) {
+                int64_t block = blockIdx.x;
+                int put = 0;
+                auto announce = [&](const Item& it) {
+                    const int i = put % kItems;
+                    if (put >= kItems && !mbar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
+                    items[i] = it;
+                    mbar_arrive(&bars[IFULL + i]);
+                    ++put;
+                    return true;
+                };
+                for (int asked = 0;; ++asked) {
+                    Item it;
+                    it.scan = 0;
+                    unsigned b = (unsigned)block;
+                    while (b >= prm.scan[it.scan].blocks) b -= prm.scan[it.scan++].blocks;
+                    const ScanArgs& a = prm.scan[it.scan].a;
+                    const unsigned ndvb = (a.Dv + DVB - 1) / DVB;
+                    it.dv0 = (int)(b % ndvb) * DVB;
+                    it.h = (int)(b / ndvb % a.H);
+                    it.slot = (int)(b / (ndvb * (unsigned)a.H));
+                    if (sorted) it.slot = order[it.slot];
+                    const Segment g = segment_of(a, it.slot);
+                    if (a.cu && a.seg_len == 0 && it.h == 0 && it.dv0 == 0 && !sequence_span(a, it.slot).ok)
+                        atomicOr(a.err, kErrBadSeqlens);
+                    it.seq = (int)g.seq;
+                    it.row0 = (int)g.row0;
+                    it.nc = (int)((g.n + C - 1) / C);
+                    it.last = (int)(g.n - (int64_t)(it.nc - 1) * C);
+                    it.l = a.log_decay[it.h];
+                    it.rev = a.reverse;
+                    // What the second part leaves (2^-16) shows in a state that the caller gets unless at least d rows follow
+                    // with e^{l d} < 2^-8: l d < -6.
+                    it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
+                               : it.l < 0.f ? (int)fminf(6.f / (C * -it.l) + 2.f, 1e9f)
+                                            : 1 << 30;
+                    // the next block is taken only when this item's last three loads are due: early enough to be announced
+                    // by then, late enough that none waits here while another SM is idle
+                    bool ok = !g.ok || (announce(it) && mbar_wait(&bars[LASTLOAD], (put - 1) & 1, stop, kItemWait));
+                    if (ok) {
+                        mbar_arrive_expect_tx(&bars[NEXT], 16);
+                        ask_next_block(answer, &bars[NEXT]);
+                        ok = mbar_wait(&bars[NEXT], asked & 1, nullptr);
+                        block = next_block(answer);
+                        fence_async_smem();  // read before the next answer is written
+                    }
+                    if (!ok) *stop = 1;
+                    if (!ok || block < 0) break;
+                }
+                Item end;
+                end.scan = -1;
+                if (!announce(end)) *stop = 1;
+            }
         } else if (warp == kWarpTma && lane == 0) {
             // ---- tile loads ----
             Ring ring;
