@@ -21,13 +21,15 @@
 // lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits) where what the second leaves would show in a
 // state that the caller gets, so that such a state is as exact as fp32 sums.
 //
-// 24 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
+// 28 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
-//   8-15  V' of the next chunk (shared memory -> shared memory), then S of this one (TMEM -> registers ->
-//         shared memory), 32 channels each; the same threads zero the rows behind a sequence's end in K and V
-//   16-19 o: TMEM -> registers -> global, a row per thread in 32-byte stores
-//   20    TMA: K, V, Q of a chunk, two or three stages
-//   21    tcgen05.mma (22 and 23 only complete the warpgroup)
+//   8-15  V' (shared memory -> shared memory), 32 channels each; the same threads zero the rows behind a sequence's end
+//         in K and V
+//   16-23 S: TMEM -> registers -> shared memory, and o: TMEM -> registers -> global, a row per thread in 32-byte stores;
+//         32 channels each
+//   24    TMA: K, V, Q of a chunk, two or three stages
+//   25    tcgen05.mma
+//   26    the CTA's items (27 only completes the warpgroup)
 // Bound by HBM where there are enough heads: Q, K, V are read once (Q and K once for each 64 value
 // channels, the second time from L2), o written once.
 #include "ssd_common.cuh"
@@ -44,20 +46,21 @@ namespace {
 using namespace ssd::sm100;
 
 constexpr int C = 128, DVB = 64, kHalf = 32;
-constexpr int kWarpOut = 16, kWarpTma = 20, kWarpMma = 21, kWarpItem = 22, kThreads = 24 * 32;
+constexpr int kWarpOut = 16, kWarpTma = 24, kWarpMma = 25, kWarpItem = 26, kThreads = 28 * 32;
+constexpr int kRegisters = 72;  // of a thread at launch
 constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
 constexpr uint32_t OFF_VP = 10 * kBox;           // behind the stages; V': up to three boxes
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
-constexpr uint32_t OFF_STOP = OFF_BAR + 240, OFF_TMEM = OFF_BAR + 248, OFF_ANSWER = OFF_BAR + 256, OFF_ITEM = OFF_BAR + 288;
+constexpr uint32_t OFF_STOP = OFF_BAR + 256, OFF_TMEM = OFF_BAR + 264, OFF_ANSWER = OFF_BAR + 272, OFF_ITEM = OFF_BAR + 288;
 constexpr uint32_t OFF_ORDER = OFF_BAR + 512;
 constexpr int kSorted = 64;   // packed sequences that are taken longest first
 constexpr uint32_t kSmemBytes = OFF_ORDER + kSorted + 1024;  // + alignment of the base
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
 constexpr int kStages = 3;  // at most
-enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, PFULL = 12, PREADY, VREADY, DSFULL, SREADY, Y2DONE, YFULL, EPI, MMADONE,
-           NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
-static_assert(kBars * 8 <= 240, "the barriers' place");
+enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, DSFULL = 12, DSREAD = 14, PFULL = 16, PREADY, VREADY, SREADY, Y2DONE, YFULL,
+           EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
+static_assert(kBars * 8 <= 256, "the barriers' place");
 // TMEM columns: scores (their bf16 form takes the place of each 16), Y1, Y2, dS (two buffers of two parts)
 constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
 
@@ -72,9 +75,8 @@ struct Params {
     Scan scan[kMaxScans];
 };
 
-// Moves registers between warpgroups: of the 768 x 80 launched with, 2 x 128 x 32 go to the scores, given by
-// V' and S (2 x 128 x 8), the outputs (128 x 16) and the last warpgroup (128 x 32); where there are no scores,
-// V' and S take 24 of what the scores' warps (256 x 40) and the other two (128 x (16 + 32)) give.
+// Moves registers between warpgroups.  Launched with 896 x 72; with outputs 256 x 112 (scores) + 256 x 40 (V') + 256 x 80
+// (S and outputs) + 128 x 40, without them 256 x 40 + 256 x 64 + 256 x 104 + 128 x 56: never more than launched.
 template <int N> __device__ __forceinline__ void regs_more() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -247,10 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY ? 8
-                                    : i == EPI                                ? 4
-                                    : i >= IEMPTY                             ? (kOut ? 22 : 10)  // roles that read an item
-                                                                              : 1);
+                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY || i == EPI || i == DSREAD || i == DSREAD + 1 ? 8
+                                    : i >= IEMPTY ? (kOut ? 26 : 18)  // warps that read an item
+                                                  : 1);
             *stop = 0;
             fence_mbar_init();
         }
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };
 
     if (warp >= kWarpTma) {
-        regs_fewer<48>();
+        regs_fewer<kOut ? 40 : 56>();
         if (warp == kWarpItem) {
             // ---- items ----
             const ScanArgs& call = prm.scan[0].a;  // a launch's scans have the same sequences
@@ -432,10 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         }
                         __syncwarp();
                     }
-                    // dS = K^T V' (its buffer was read before the S that the last Y2 waited for): the parts lie one box
+                    // dS = K^T V' (its buffer was read before the S that the last Y2 waited for, if there is one): the parts lie one box
                     // behind the other, the first two are one product with 64 columns each, so that K is read once; the
                     // third adds to the second
-                    if (!(ok = warp_wait(&bars[VREADY], cc & 1, stop))) break;
+                    ok = warp_wait(&bars[VREADY], cc & 1, stop) &&
+                         (kOut || cc < 2 || warp_wait(&bars[DSREAD + (cc & 1)], ((cc >> 1) - 1) & 1, stop));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t dKt = sw128_desc(tk, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
                     if (elect_one()) {
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             for (int k = 0; k < 8; ++k)
                                 mma_bf16(ds + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
                         }
-                        mma_commit(&bars[DSFULL]);
+                        mma_commit(&bars[DSFULL + (cc & 1)]);
                         mma_commit(&bars[KFREE + s]);
                     }
                     __syncwarp();
@@ -569,48 +572,42 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) *stop = 1;
         }
     } else if (warp < kWarpOut) {
-        // ---- V' and S: tile row / key row `row`, 32 of the 64 channels ----
-        if (kOut) regs_fewer<72>();
-        else regs_more<104>();
+        // ---- V': tile row `row`, 32 of the 64 channels ----
+        regs_fewer<kOut ? 40 : 64>();
         const int half = (warp >> 2) & 1;
-        float S[kHalf];
         int cc = 0;
         Ring ring;
         const Item* it;
         bool ok = true;
-        auto publish = [&] {  // the bf16 copy that Y2 reads
-            uint8_t* p = sm + OFF_S;
-#pragma unroll
-            for (int i = 0; i < kHalf / 8; ++i)
-                *reinterpret_cast<uint4*>(p + sw128_off(row, half * 4 + i)) =
-                    make_uint4(pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
-                               pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
-            fence_async_smem();
-            warp_arrive(&bars[SREADY], lane);
-        };
-        // the item is read from its place in the ring wherever it is needed, not kept in registers
         for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
-            ring.cut(prm.scan[it->scan].a.Dk, kOut);
-            auto rows = [&](int c) { return rows_of(place_of(it->rev, it->nc, c), it->nc, it->last); };
+            const ScanArgs& a = prm.scan[it->scan].a;
+            ring.cut(a.Dk, kOut);
+            const int nc = it->nc, last = it->last, third = it->third;
+            const float l = it->l, w_scale = a.w_scale;
+            const bool rev = a.reverse;
+            leave(k, true);
             // weight of tile row `row` in the state behind a chunk of n rows
-            auto weight = [&](int n) {
-                return row < n ? prm.scan[it->scan].a.w_scale * decay_pow(it->l, it->rev ? row + 1 : n - 1 - row) : 0.f;
-            };
-            const float w_full = weight(C), decay_full = decay_pow(it->l, C);
-            auto split = [&](int c, const Ring& at) {  // V' of chunk c; zeros behind the sequence's end
-                const int n = rows(c);
-                const bool three = kMaxParts == 3 && it->nc - c <= it->third;
-                uint8_t* tv = sm + at.v(kOut);
-                const float wr = n == C ? w_full : weight(n);
-                if (row >= n) {
+            auto weight = [&](int n) { return row < n ? w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row) : 0.f; };
+            const float w_full = weight(C);
+            for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
+                const int n = rows_of(place_of(rev, nc, c), nc, last);
+                const bool three = kMaxParts == 3 && nc - c <= third;
+                const float w = n == C ? w_full : weight(n);
+                ok = warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
+                if (!ok) break;
+                uint8_t* tv = sm + ring.v(kOut);
+                if (row >= n) {  // behind the sequence's end: zeros
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t o = sw128_off(row, i);
                         const uint4 z = make_uint4(0, 0, 0, 0);
-                        if (half < at.kb) *reinterpret_cast<uint4*>(sm + at.k(kOut) + half * kBox + o) = z;
+                        if (half < ring.kb) *reinterpret_cast<uint4*>(sm + ring.k(kOut) + half * kBox + o) = z;
                         if (i / 4 == half) *reinterpret_cast<uint4*>(tv + o) = z;
                     }
                 }
+                // the product that reads the last V' is complete
+                ok = cc == 0 || warp_wait(&bars[DSFULL + ((cc - 1) & 1)], ((cc - 1) >> 1) & 1, stop);
+                if (!ok) break;
 #pragma unroll 2
                 for (int i = 0; i < kHalf / 8; ++i) {
                     const uint32_t o = sw128_off(row, half * 4 + i);
@@ -619,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     uint32_t part[kMaxParts][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(wr, wr));
+                        float2 f = __fmul2_rn(make_float2(bf_lo(in[k]), bf_hi(in[k])), make_float2(w, w));
                         // a part is the upper half of the word: 8 bits cut off, the rest exact
 #pragma unroll
                         for (int t = 0; t < kMaxParts; ++t) {
@@ -636,7 +633,30 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 }
                 fence_async_smem();
                 warp_arrive(&bars[VREADY], lane);
-            };
+            }
+        }
+        if (!ok) *stop = 1;
+    } else {
+        // ---- S: key row `row`, and the outputs: tile row `row`; 32 of the 64 channels ----
+        regs_more<kOut ? 80 : 104>();
+        const int half = (warp >> 2) & 1;
+        float S[kHalf];
+        int cc = 0;
+        const Item* it;
+        bool ok = true;
+        auto publish = [&] {  // the bf16 copy that Y2 reads
+            uint8_t* p = sm + OFF_S;
+#pragma unroll
+            for (int i = 0; i < kHalf / 8; ++i)
+                *reinterpret_cast<uint4*>(p + sw128_off(row, half * 4 + i)) =
+                    make_uint4(pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
+                               pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
+            fence_async_smem();
+            warp_arrive(&bars[SREADY], lane);
+        };
+        // the item is read from its place in the ring wherever it is needed, not kept in registers
+        for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+            const float decay_full = decay_pow(it->l, C);
             // this row of the state, where it is kept: among the sequences' or the segments'
             auto state_row = [&](const float* base, bool transposed) {
                 const ScanArgs& a = prm.scan[it->scan].a;
@@ -645,14 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                        (transposed ? (size_t)d0 * a.Dk + row : (size_t)row * a.Dv + d0);
             };
             const int live = prm.scan[it->scan].a.Dv - (it->dv0 + half * kHalf);  // channels of this half
-            if (it->nc > 0) {
-                ok = warp_wait(&bars[FULL + ring.s], ring.phase(), stop);
-                if (ok) split(0, ring);
-            }
 #pragma unroll
             for (int d = 0; d < kHalf; ++d) S[d] = 0.f;
-            if (kMode != kStates) {
+            float e_full = 0.f;  // the outputs' coefficient of S
+            if (kOut) {
                 const ScanArgs& a = prm.scan[it->scan].a;
+                e_full = a.inter_scale * decay_pow(it->l, it->rev ? C - 1 - row : row + 1);
                 const float* init = kMode == kOutputs ? a.seg_state : a.init;
                 const bool init_t = kMode == kWhole ? a.init_t : a.seg_t;
                 if (init && row < a.Dk) {
@@ -670,49 +688,72 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             }
                     }
                 }
-                if (ok && it->nc > 0) {  // over the S that the item before left, once it has been read
+                if (it->nc > 0) {  // over the S that the item before left, once it has been read
                     ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
                     if (ok) publish();
                 }
             }
-            for (int c = 0; ok && c < it->nc; ++c, ++cc, ring.step()) {
-                if (!(ok = warp_wait(&bars[DSFULL], cc & 1, stop))) break;
-                // V' of the next chunk and S of this one are free of one another: the next V' first if its tile is
-                // here, so that its product runs while S is updated
-                const bool more = c + 1 < it->nc;
-                Ring then = ring;
-                then.step();
-                const bool ahead = more && __all_sync(0xffffffffu, mbar_test(&bars[FULL + then.s], then.phase()));
-#pragma unroll 1
-                for (int step = 0; ok && step < 2; ++step) {
-                    if ((step == 0) == ahead) {
-                        if (!more) continue;
-                        ok = warp_wait(&bars[FULL + then.s], then.phase(), stop);
-                        if (ok) split(c + 1, then);
-                        continue;
+            for (int c = 0; ok && c < it->nc; ++c, ++cc) {
+                if (!(ok = warp_wait(&bars[DSFULL + (cc & 1)], (cc >> 1) & 1, stop))) break;
+                tc_fence_after();
+                const int place = place_of(it->rev, it->nc, c), n = rows_of(place, it->nc, it->last);
+                const float decay = n == C ? decay_full : decay_pow(it->l, n);
+#pragma unroll
+                for (int b = 0; b < kHalf / 8; ++b) {
+                    const uint32_t col = lane_base + COL_DS + (cc & 1) * 128 + half * kHalf + b * 8;
+                    float x[8], y[8];
+                    tmem_ld8(col, x);
+                    tmem_ld8(col + 64, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
+                        const float2 f = __ffma2_rn(make_float2(decay, decay), make_float2(S[b * 8 + j], S[b * 8 + j + 1]), d);
+                        S[b * 8 + j] = f.x;
+                        S[b * 8 + j + 1] = f.y;
                     }
+                }
+                tc_fence_before();
+                if constexpr (!kOut) {
+                    warp_arrive(&bars[DSREAD + (cc & 1)], lane);
+                } else {
+                    if (c + 1 < it->nc) {
+                        if (!(ok = warp_wait(&bars[Y2DONE], cc & 1, stop))) break;
+                        publish();
+                    }
+                    if (!(ok = warp_wait(&bars[YFULL], cc & 1, stop))) break;
                     tc_fence_after();
-                    const int n = rows(c);
-                    const float e = n == C ? decay_full : decay_pow(it->l, n);
+                    const ScanArgs& a = prm.scan[it->scan].a;
+                    const float e = n == C  ? e_full
+                                    : row < n ? a.inter_scale * decay_pow(it->l, it->rev ? n - 1 - row : row + 1)
+                                              : 0.f;
+                    // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
+                    const int esize = a.o_f32 ? 4 : 2, stored = row < n ? live : 0;
+                    const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+                    uint8_t* dst = static_cast<uint8_t*>(a.o) +
+                                   (((int64_t)it->row0 + place * C + row) * a.H * a.Dv + (int64_t)it->h * a.Dv + it->dv0 +
+                                    half * kHalf) * esize;
 #pragma unroll
-                    for (int b = 0; b < kHalf / 8; ++b) {  // 8 at a time: this is where the role's registers run out
-                        const uint32_t col = lane_base + COL_DS + (cc & 1) * 128 + half * kHalf + b * 8;
-                        float x[8], y[8];
-                        tmem_ld8(col, x);
-                        tmem_ld8(col + 64, y);
+                    for (int b = 0; b < kHalf / 16; ++b) {
+                        float x[16], y[16];
+                        tmem_ld16(lane_base + COL_Y1 + half * kHalf + b * 16, x);
+                        tmem_ld16(lane_base + COL_Y2 + half * kHalf + b * 16, y);
                         tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            const float2 d = __fadd2_rn(make_float2(x[j], x[j + 1]), make_float2(y[j], y[j + 1]));
-                            const float2 f = __ffma2_rn(make_float2(e, e), make_float2(S[b * 8 + j], S[b * 8 + j + 1]), d);
-                            S[b * 8 + j] = f.x;
-                            S[b * 8 + j + 1] = f.y;
+                        if (b == kHalf / 16 - 1) {
+                            tc_fence_before();
+                            warp_arrive(&bars[EPI], lane);
                         }
-                    }
-                    tc_fence_before();
-                    if (kOut && more) {
-                        ok = warp_wait(&bars[Y2DONE], cc & 1, stop);
-                        if (ok) publish();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 f =
+                                __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
+                            x[j] = f.x;
+                            x[j + 1] = f.y;
+                        }
+                        if (a.o_f32)
+                            store16(reinterpret_cast<float*>(dst) + b * 16, x, stored - b * 16, wide);
+                        else
+                            store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, stored - b * 16, wide);
                     }
                 }
             }
@@ -729,59 +770,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             leave(k, true);
         }
         if (!ok) *stop = 1;
-    } else {
-        regs_fewer<64>();
-        if (kOut) {
-            // ---- outputs: tile row `row` ----
-            int cc = 0;
-            const Item* it;
-            bool ok = true;
-            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
-                const ScanArgs& a = prm.scan[it->scan].a;
-                const int nc = it->nc, last = it->last, nv = min(DVB, a.Dv - it->dv0);
-                const float l = it->l;
-                const bool rev = a.reverse;
-                const int64_t row_elems = (int64_t)a.H * a.Dv;
-                const int64_t first = ((int64_t)it->row0 + row) * row_elems + (int64_t)it->h * a.Dv + it->dv0;
-                leave(k, true);
-                auto coefficient = [&](int n) { return a.inter_scale * decay_pow(l, rev ? n - 1 - row : row + 1); };
-                const float e_full = coefficient(C);
-                // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
-                const int esize = a.o_f32 ? 4 : 2;
-                const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
-                for (int c = 0; ok && c < nc; ++c, ++cc) {
-                    const int place = place_of(rev, nc, c), n = rows_of(place, nc, last);
-                    const float e = n == C ? e_full : row < n ? coefficient(n) : 0.f;
-                    if (!(ok = warp_wait(&bars[YFULL], cc & 1, stop))) break;
-                    tc_fence_after();
-                    uint8_t* dst = static_cast<uint8_t*>(a.o) + (first + (int64_t)place * C * row_elems) * esize;
-                    const int live = row < n ? nv : 0;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float x[16], y[16];
-                        tmem_ld16(lane_base + COL_Y1 + b * 16, x);
-                        tmem_ld16(lane_base + COL_Y2 + b * 16, y);
-                        tmem_wait_ld();
-                        if (b == 3) {
-                            tc_fence_before();
-                            warp_arrive(&bars[EPI], lane);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const float2 f =
-                                __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
-                            x[j] = f.x;
-                            x[j + 1] = f.y;
-                        }
-                        if (a.o_f32)
-                            store16(reinterpret_cast<float*>(dst) + b * 16, x, live - b * 16, wide);
-                        else
-                            store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, live - b * 16, wide);
-                    }
-                }
-            }
-            if (!ok) *stop = 1;
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -823,6 +811,12 @@ bool make_map(CUtensorMap* m, const void* base, int width, int heads, int64_t ro
 template <int kMode> cudaError_t launch(const Params& prm, unsigned blocks, cudaStream_t st) {
     const cudaError_t e = allow_smem<scan_tc_kernel<kMode>>((int)kSmemBytes);
     if (e != cudaSuccess) return e;
+    // the warpgroups' shares add up to what 72 registers a thread give; from fewer a warpgroup would wait for ever
+    static const int regs = [] {
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, scan_tc_kernel<kMode>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs != kRegisters) return cudaErrorInvalidConfiguration;
     scan_tc_kernel<kMode><<<blocks, kThreads, kSmemBytes, st>>>(prm);
     return cudaGetLastError();
 }
