@@ -266,8 +266,8 @@ int64_t segment_rows(int64_t batch, int64_t L, int64_t rows, bool packed, bool b
     if (batch == 0 || rows == 0) return 0;
     const Cost k = cost_of(bf16, Dk);
     const double mean = (double)rows / batch;
-    // the longest of a packed batch is not known here; three times the mean is usual for prompts
-    const double longest = packed ? fmin((double)rows, 3.0 * mean) : (double)L;
+    // the longest of a packed batch is not known here; four times the mean is usual for prompts
+    const double longest = packed ? fmin((double)rows, 4.0 * mean) : (double)L;
     auto waves = [&](double n, int launches) {
         if (k.together) launches = 1;
         const double w = n / launches / k.slots;

@@ -15,10 +15,13 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 128, C = 32, DVB = 64;
-constexpr int PV = DVB + 4, PP = C + 4;  // padded row lengths (floats), 16-byte multiples
+// Row lengths (floats): K's rows are read by lanes of different rows, so they are padded; the scores take the place of Q,
+// which has been read by then.  73 KB at Dk = 128: three blocks to an SM.
+constexpr int PV = DVB, PP = C + 4;
 
+template <int DKP> constexpr int q_floats() { return C * (DKP > PP ? DKP : PP); }
 template <int DKP> constexpr size_t smem_bytes() {
-    return sizeof(float) * (2 * C * (DKP + 4) + C * PV + DKP * PV + C * PP + 3 * C);
+    return sizeof(float) * (q_floats<DKP>() + C * (DKP + 4) + C * PV + DKP * PV + 2 * C);
 }
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
@@ -29,23 +32,27 @@ __device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cas
 __device__ __forceinline__ void st4(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
-    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
+// Two multiply-adds to an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 dot4(float4 a, float4 b, float2 s) {
+    return fma2(make_float2(a.z, a.w), make_float2(b.z, b.w), fma2(make_float2(a.x, a.y), make_float2(b.x, b.y), s));
 }
-__device__ __forceinline__ void axpy4(float (&o)[4], float a, float4 x) {
-    o[0] = fmaf(a, x.x, o[0]); o[1] = fmaf(a, x.y, o[1]); o[2] = fmaf(a, x.z, o[2]); o[3] = fmaf(a, x.w, o[3]);
+__device__ __forceinline__ void axpy4(float2 (&o)[2], float a, float4 x) {
+    o[0] = fma2(both(a), make_float2(x.x, x.y), o[0]);
+    o[1] = fma2(both(a), make_float2(x.z, x.w), o[1]);
 }
 
 template <int DKP, int MODE>
-__global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PK = DKP + 4, TK = DKP / 16;  // state rows of a thread
     float* sQ = sm;
-    float* sK = sQ + C * PK;
+    float* sK = sQ + q_floats<DKP>();
     float* sV = sK + C * PK;
     float* sS = sV + C * PV;
-    float* sP = sS + DKP * PV;
-    float* sPow = sP + C * PP;  // e^{l n}, n = 0 .. C
+    float* sP = sQ;
+    float* sPow = sS + DKP * PV;  // e^{l n}, n = 0 .. C
     const int tid = threadIdx.x, h = blockIdx.y, dv0 = blockIdx.z * DVB;
     const int nv = min(DVB, a.Dv - dv0);
     const Segment g = segment_of(a, blockIdx.x);
@@ -57,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
     const int s = a.reverse ? 0 : 1;
 
     const int k0 = (tid >> 3) * TK, v0 = (tid & 7) * 8;  // this thread's state rows and channels
-    float S[TK][8];
+    float2 S[TK][4];
     const size_t at_state = (size_t)a.Dk * a.Dv;
     const float* init = MODE == kOutputs ? a.seg_state + ((size_t)blockIdx.x * a.H + h) * at_state
                         : MODE == kStates || !a.init ? nullptr
@@ -68,9 +75,10 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const int kk = k0 + r, vv = v0 + c;
-            S[r][c] = init && kk < a.Dk && vv < nv
-                          ? init[init_t ? (size_t)(dv0 + vv) * a.Dk + kk : (size_t)kk * a.Dv + dv0 + vv]
-                          : 0.f;
+            const float x = init && kk < a.Dk && vv < nv
+                                ? init[init_t ? (size_t)(dv0 + vv) * a.Dk + kk : (size_t)kk * a.Dv + dv0 + vv]
+                                : 0.f;
+            (c & 1 ? S[r][c / 2].y : S[r][c / 2].x) = x;
         }
     const float* q = static_cast<const float*>(a.q) + (size_t)(h / a.gq) * a.Dk;
     const float* k = static_cast<const float*>(a.k) + (size_t)(h / a.gk) * a.Dk;
@@ -88,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
                 if (MODE != kStates) load4(q + row(r) * a.rs_q + d, x);
                 load4(k + row(r) * a.rs_k + d, y);
             }
-            if (MODE != kStates) st4(sQ + r * PK + d, x[0], x[1], x[2], x[3]);
+            if (MODE != kStates) st4(sQ + r * DKP + d, x[0], x[1], x[2], x[3]);
             st4(sK + r * PK + d, y[0], y[1], y[2], y[3]);
         }
         for (int i = tid; i < C * (DVB / 4); i += kThreads) {
@@ -100,17 +108,18 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
         if (MODE != kStates) {
 #pragma unroll
             for (int r = 0; r < TK; ++r) {
-                st4(sS + (k0 + r) * PV + v0, S[r][0], S[r][1], S[r][2], S[r][3]);
-                st4(sS + (k0 + r) * PV + v0 + 4, S[r][4], S[r][5], S[r][6], S[r][7]);
+                st4(sS + (k0 + r) * PV + v0, S[r][0].x, S[r][0].y, S[r][1].x, S[r][1].y);
+                st4(sS + (k0 + r) * PV + v0 + 4, S[r][2].x, S[r][2].y, S[r][3].x, S[r][3].y);
             }
         }
         __syncthreads();
         if (MODE != kStates) {
-            // P: rows i0, i0 + 16, columns j0 + {0, 8, 16, 24}
-            const int i0 = tid >> 3, j0 = tid & 7;
-            float p[2][4] = {};
+            // P: rows i0, i0 + 16, columns j0 + {0, 8, 16, 24}; O: rows r0 .. r0+3, channels c4 .. c4+3
+            const int i0 = tid >> 3, j0 = tid & 7, r0 = (tid >> 4) * 4, c4 = (tid & 15) * 4;
+            float2 p[2][4] = {};
+#pragma unroll 2
             for (int d = 0; d < a.Dk; d += 4) {
-                const float4 qa = lds4(sQ + i0 * PK + d), qb = lds4(sQ + (i0 + 16) * PK + d);
+                const float4 qa = lds4(sQ + i0 * DKP + d), qb = lds4(sQ + (i0 + 16) * DKP + d);
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const float4 kk = lds4(sK + (j0 + 8 * jj) * PK + d);
@@ -118,31 +127,37 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
                     p[1][jj] = dot4(qb, kk, p[1][jj]);
                 }
             }
+            float2 out[4][2] = {};
+#pragma unroll 2
+            for (int d = 0; d < a.Dk; d += 4) {
+                float4 qq[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qq[i] = lds4(sQ + (r0 + i) * DKP + d);
+                const float4 s0 = lds4(sS + d * PV + c4), s1 = lds4(sS + (d + 1) * PV + c4);
+                const float4 s2 = lds4(sS + (d + 2) * PV + c4), s3 = lds4(sS + (d + 3) * PV + c4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    axpy4(out[i], qq[i].x, s0);
+                    axpy4(out[i], qq[i].y, s1);
+                    axpy4(out[i], qq[i].z, s2);
+                    axpy4(out[i], qq[i].w, s3);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 e = both(a.inter_scale * sPow[r0 + i + s]);
+                out[i][0] = __fmul2_rn(e, out[i][0]);
+                out[i][1] = __fmul2_rn(e, out[i][1]);
+            }
+            __syncthreads();  // Q has been read
 #pragma unroll
             for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const int i = i0 + 16 * ii, j = j0 + 8 * jj;
-                    sP[i * PP + j] = j <= i ? p[ii][jj] * a.qk_scale * sPow[i - j] : 0.f;
+                    sP[i * PP + j] = j <= i ? (p[ii][jj].x + p[ii][jj].y) * a.qk_scale * sPow[i - j] : 0.f;
                 }
             __syncthreads();
-            // O: rows r0 .. r0+3, channels c4 .. c4+3
-            const int r0 = (tid >> 4) * 4, c4 = (tid & 15) * 4;
-            float out[4][4] = {}, in[4][4] = {};
-            for (int d = 0; d < a.Dk; d += 4) {
-                float4 qq[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qq[i] = lds4(sQ + (r0 + i) * PK + d);
-                const float4 s0 = lds4(sS + d * PV + c4), s1 = lds4(sS + (d + 1) * PV + c4);
-                const float4 s2 = lds4(sS + (d + 2) * PV + c4), s3 = lds4(sS + (d + 3) * PV + c4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    axpy4(in[i], qq[i].x, s0);
-                    axpy4(in[i], qq[i].y, s1);
-                    axpy4(in[i], qq[i].z, s2);
-                    axpy4(in[i], qq[i].w, s3);
-                }
-            }
             for (int j = 0; j < r0 + 4; j += 4) {
                 float4 pp[4];
 #pragma unroll
@@ -158,31 +173,26 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (r0 + i < n && c4 < nv) {
-                    const float e = a.inter_scale * sPow[r0 + i + s];
-                    float* dst = o + row(r0 + i) * (int64_t)a.H * a.Dv + c4;
-                    st4(dst, fmaf(e, in[i][0], out[i][0]), fmaf(e, in[i][1], out[i][1]), fmaf(e, in[i][2], out[i][2]),
-                         fmaf(e, in[i][3], out[i][3]));
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (r0 + i < n && c4 < nv)
+                    st4(o + row(r0 + i) * (int64_t)a.H * a.Dv + c4, out[i][0].x, out[i][0].y, out[i][1].x, out[i][1].y);
         }
         // S: rows behind n are zero in shared memory
-        const float e = sPow[n];
+        const float2 e = both(sPow[n]);
 #pragma unroll
         for (int r = 0; r < TK; ++r)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) S[r][c] *= e;
+            for (int c = 0; c < 4; ++c) S[r][c] = __fmul2_rn(e, S[r][c]);
+#pragma unroll 2
         for (int j = 0; j < n; ++j) {
             const float w = a.w_scale * sPow[n - j - s];
             const float4 x = lds4(sV + j * PV + v0), y = lds4(sV + j * PV + v0 + 4);
+            const float2 v2[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)};
 #pragma unroll
             for (int r = 0; r < TK; ++r) {
-                const float kk = w * sK[j * PK + k0 + r];
-                S[r][0] = fmaf(kk, x.x, S[r][0]); S[r][1] = fmaf(kk, x.y, S[r][1]);
-                S[r][2] = fmaf(kk, x.z, S[r][2]); S[r][3] = fmaf(kk, x.w, S[r][3]);
-                S[r][4] = fmaf(kk, y.x, S[r][4]); S[r][5] = fmaf(kk, y.y, S[r][5]);
-                S[r][6] = fmaf(kk, y.z, S[r][6]); S[r][7] = fmaf(kk, y.w, S[r][7]);
+                const float2 kk = both(w * sK[j * PK + k0 + r]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[r][c] = fma2(kk, v2[c], S[r][c]);
             }
         }
     }
@@ -194,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) scan_simt_kernel(ScanArgs a) {
         for (int r = 0; r < TK; ++r)
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (k0 + r < a.Dk && v0 + c < nv) fin[(size_t)(k0 + r) * a.Dv + dv0 + v0 + c] = S[r][c];
+                if (k0 + r < a.Dk && v0 + c < nv)
+                    fin[(size_t)(k0 + r) * a.Dv + dv0 + v0 + c] = c & 1 ? S[r][c / 2].y : S[r][c / 2].x;
     }
 }
 
