@@ -256,7 +256,7 @@ struct Cost {
 };
 Cost cost_of(bool bf16, int Dk) {
     if (bf16) return Cost{5.0, 2.0 / 128, 1.2 / 128, 6.0, 5e6, 148.0, 256, true};
-    const double row = 0.06 + 0.0024 * Dk;
+    const double row = 0.06 + 0.0021 * Dk;
     return Cost{5.0, row, 0.45 * row, 10.0, 2.5e6, Dk > 64 ? 220.0 : 450.0, 32, false};
 }
 // Rows of a segment, or 0: whole sequences.  `blocks`: blocks of the output pass for each sequence, of `scans` scans;
@@ -281,9 +281,12 @@ int64_t segment_rows(int64_t batch, int64_t L, int64_t rows, bool packed, bool b
     for (; m >= k.least && m < longest; m /= 2) {  // the longest that is not 10 % worse than a shorter one
         const double slots = packed ? rows / (double)m + 0.5 * batch : batch * ceil((double)L / m);
         const double bytes = slots * H * Dk * Dv * 4 * 4 * state_scans;  // written, read and written, read
-        const double part = fmin((double)m, mean);
-        const double t = waves(slots * state_blocks, state_scans) * (k.start + part * k.state_row) +
-                         waves(slots * blocks, scans) * (k.start + part * k.row) + k.extra + bytes / k.state_rate;
+        const double part = fmin((double)m, mean), most = fmin((double)m, longest);
+        auto pass = [&](double n, int of, double per_row) {
+            return fmax(waves(n, of) * (k.start + part * per_row), (k.together ? 1 : of) * (k.start + most * per_row));
+        };
+        const double t = pass(slots * state_blocks, state_scans, k.state_row) + pass(slots * blocks, scans, k.row) + k.extra +
+                         bytes / k.state_rate;
         if (t < 0.9 * best) {
             best = t;
             seg = m;

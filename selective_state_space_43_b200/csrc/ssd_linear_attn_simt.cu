@@ -14,9 +14,9 @@ namespace ssd {
 namespace la {
 namespace {
 
-constexpr int kThreads = 128, C = 32, DVB = 64;
+constexpr int kGroup = 128, C = 32, DVB = 64;
 // Row lengths (floats): K's rows are read by lanes of different rows, so they are padded; the scores take the place of Q,
-// which has been read by then.  73 KB at Dk = 128: three blocks to an SM.
+// which has been read by then.
 constexpr int PV = DVB, PP = C + 4;
 
 template <int DKP> constexpr int q_floats() { return C * (DKP > PP ? DKP : PP); }
@@ -43,8 +43,15 @@ __device__ __forceinline__ void axpy4(float2 (&o)[2], float a, float4 x) {
     o[1] = fma2(both(a), make_float2(x.z, x.w), o[1]);
 }
 
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }  // the outputs' group
+
+// Two groups of 128 threads, the outputs of a chunk and its state side by side (both start from the state before it); for
+// states alone the second group is the block.
+template <int MODE> constexpr int threads() { return MODE == kStates ? kGroup : 2 * kGroup; }
+
 template <int DKP, int MODE>
-__global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
+__global__ void __launch_bounds__(threads<MODE>(), 2) scan_simt_kernel(ScanArgs a) {
+    constexpr int kThreads = threads<MODE>();
     extern __shared__ __align__(16) float sm[];
     constexpr int PK = DKP + 4, TK = DKP / 16;  // state rows of a thread
     float* sQ = sm;
@@ -53,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
     float* sS = sV + C * PV;
     float* sP = sQ;
     float* sPow = sS + DKP * PV;  // e^{l n}, n = 0 .. C
-    const int tid = threadIdx.x, h = blockIdx.y, dv0 = blockIdx.z * DVB;
+    const int tid = threadIdx.x, t = tid % kGroup, h = blockIdx.y, dv0 = blockIdx.z * DVB;
     const int nv = min(DVB, a.Dv - dv0);
     const Segment g = segment_of(a, blockIdx.x);
     if (a.cu && tid == 0 && h == 0 && blockIdx.z == 0 && !sequence_span(a, g.seq).ok)
@@ -63,38 +70,17 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
     if (tid <= C) sPow[tid] = tid == 0 ? 1.f : expf(l * (float)tid);
     const int s = a.reverse ? 0 : 1;
 
-    const int k0 = (tid >> 3) * TK, v0 = (tid & 7) * 8;  // this thread's state rows and channels
-    float2 S[TK][4];
-    const size_t at_state = (size_t)a.Dk * a.Dv;
-    const float* init = MODE == kOutputs ? a.seg_state + ((size_t)blockIdx.x * a.H + h) * at_state
-                        : MODE == kStates || !a.init ? nullptr
-                                                     : a.init + ((size_t)g.seq * a.H + h) * at_state;
-    const bool init_t = MODE == kWhole ? a.init_t : a.seg_t;
-#pragma unroll
-    for (int r = 0; r < TK; ++r)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int kk = k0 + r, vv = v0 + c;
-            const float x = init && kk < a.Dk && vv < nv
-                                ? init[init_t ? (size_t)(dv0 + vv) * a.Dk + kk : (size_t)kk * a.Dv + dv0 + vv]
-                                : 0.f;
-            (c & 1 ? S[r][c / 2].y : S[r][c / 2].x) = x;
-        }
     const float* q = static_cast<const float*>(a.q) + (size_t)(h / a.gq) * a.Dk;
     const float* k = static_cast<const float*>(a.k) + (size_t)(h / a.gk) * a.Dk;
     const float* v = static_cast<const float*>(a.v) + (size_t)(h / a.gv) * a.Dv + dv0;
-    float* o = static_cast<float*>(a.o) + (size_t)h * a.Dv + dv0;
-
-    for (int64_t c0 = 0; c0 < g.n; c0 += C) {
-        const int n = (int)min((int64_t)C, g.n - c0);
-        auto row = [&](int i) { return a.reverse ? g.row0 + g.n - 1 - (c0 + i) : g.row0 + c0 + i; };
-        __syncthreads();  // the last chunk's reads are done
+    auto row = [&](int64_t c0, int i) { return a.reverse ? g.row0 + g.n - 1 - (c0 + i) : g.row0 + c0 + i; };
+    auto load_tiles = [&](int64_t c0, int n) {  // both groups
         for (int i = tid; i < C * (DKP / 4); i += kThreads) {
             const int r = i / (DKP / 4), d = (i % (DKP / 4)) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
             if (r < n && d < a.Dk) {
-                if (MODE != kStates) load4(q + row(r) * a.rs_q + d, x);
-                load4(k + row(r) * a.rs_k + d, y);
+                if (MODE != kStates) load4(q + row(c0, r) * a.rs_q + d, x);
+                load4(k + row(c0, r) * a.rs_k + d, y);
             }
             if (MODE != kStates) st4(sQ + r * DKP + d, x[0], x[1], x[2], x[3]);
             st4(sK + r * PK + d, y[0], y[1], y[2], y[3]);
@@ -102,20 +88,20 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
         for (int i = tid; i < C * (DVB / 4); i += kThreads) {
             const int r = i / (DVB / 4), d = (i % (DVB / 4)) * 4;
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r < n && d < nv) load4(v + row(r) * a.rs_v + d, x);
+            if (r < n && d < nv) load4(v + row(c0, r) * a.rs_v + d, x);
             st4(sV + r * PV + d, x[0], x[1], x[2], x[3]);
         }
-        if (MODE != kStates) {
-#pragma unroll
-            for (int r = 0; r < TK; ++r) {
-                st4(sS + (k0 + r) * PV + v0, S[r][0].x, S[r][0].y, S[r][1].x, S[r][1].y);
-                st4(sS + (k0 + r) * PV + v0 + 4, S[r][2].x, S[r][2].y, S[r][3].x, S[r][3].y);
-            }
-        }
-        __syncthreads();
-        if (MODE != kStates) {
-            // P: rows i0, i0 + 16, columns j0 + {0, 8, 16, 24}; O: rows r0 .. r0+3, channels c4 .. c4+3
-            const int i0 = tid >> 3, j0 = tid & 7, r0 = (tid >> 4) * 4, c4 = (tid & 15) * 4;
+    };
+
+    if (MODE != kStates && tid < kGroup) {
+        // ---- outputs.  P: rows i0, i0 + 16, columns j0 + {0, 8, 16, 24}; O: rows r0 .. r0+3, channels c4 .. c4+3
+        const int i0 = t >> 3, j0 = t & 7, r0 = (t >> 4) * 4, c4 = (t & 15) * 4;
+        float* o = static_cast<float*>(a.o) + (size_t)h * a.Dv + dv0;
+        for (int64_t c0 = 0; c0 < g.n; c0 += C) {
+            const int n = (int)min((int64_t)C, g.n - c0);
+            __syncthreads();  // the last chunk's reads are done
+            load_tiles(c0, n);
+            __syncthreads();
             float2 p[2][4] = {};
 #pragma unroll 2
             for (int d = 0; d < a.Dk; d += 4) {
@@ -149,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
                 out[i][0] = __fmul2_rn(e, out[i][0]);
                 out[i][1] = __fmul2_rn(e, out[i][1]);
             }
-            __syncthreads();  // Q has been read
+            group_sync();  // Q has been read
 #pragma unroll
             for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -157,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
                     const int i = i0 + 16 * ii, j = j0 + 8 * jj;
                     sP[i * PP + j] = j <= i ? (p[ii][jj].x + p[ii][jj].y) * a.qk_scale * sPow[i - j] : 0.f;
                 }
-            __syncthreads();
+            group_sync();
             for (int j = 0; j < r0 + 4; j += 4) {
                 float4 pp[4];
 #pragma unroll
@@ -175,9 +161,43 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (r0 + i < n && c4 < nv)
-                    st4(o + row(r0 + i) * (int64_t)a.H * a.Dv + c4, out[i][0].x, out[i][0].y, out[i][1].x, out[i][1].y);
+                    st4(o + row(c0, r0 + i) * (int64_t)a.H * a.Dv + c4, out[i][0].x, out[i][0].y, out[i][1].x,
+                        out[i][1].y);
         }
-        // S: rows behind n are zero in shared memory
+        return;
+    }
+
+    // ---- the state: rows k0 .. , channels v0 .. v0+7
+    const int k0 = (t >> 3) * TK, v0 = (t & 7) * 8;
+    const size_t at_state = (size_t)a.Dk * a.Dv;
+    const float* init = MODE == kOutputs ? a.seg_state + ((size_t)blockIdx.x * a.H + h) * at_state
+                        : MODE == kStates || !a.init ? nullptr
+                                                     : a.init + ((size_t)g.seq * a.H + h) * at_state;
+    const bool init_t = MODE == kWhole ? a.init_t : a.seg_t;
+    float2 S[TK][4];
+#pragma unroll
+    for (int r = 0; r < TK; ++r)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int kk = k0 + r, vv = v0 + c;
+            const float x = init && kk < a.Dk && vv < nv
+                                ? init[init_t ? (size_t)(dv0 + vv) * a.Dk + kk : (size_t)kk * a.Dv + dv0 + vv]
+                                : 0.f;
+            (c & 1 ? S[r][c / 2].y : S[r][c / 2].x) = x;
+        }
+    for (int64_t c0 = 0; c0 < g.n; c0 += C) {
+        const int n = (int)min((int64_t)C, g.n - c0);
+        __syncthreads();
+        load_tiles(c0, n);
+        if (MODE != kStates) {
+#pragma unroll
+            for (int r = 0; r < TK; ++r) {
+                st4(sS + (k0 + r) * PV + v0, S[r][0].x, S[r][0].y, S[r][1].x, S[r][1].y);
+                st4(sS + (k0 + r) * PV + v0 + 4, S[r][2].x, S[r][2].y, S[r][3].x, S[r][3].y);
+            }
+        }
+        __syncthreads();
+        // rows behind n are zero in shared memory
         const float2 e = both(sPow[n]);
 #pragma unroll
         for (int r = 0; r < TK; ++r)
@@ -188,9 +208,20 @@ __global__ void __launch_bounds__(kThreads, 3) scan_simt_kernel(ScanArgs a) {
             const float w = a.w_scale * sPow[n - j - s];
             const float4 x = lds4(sV + j * PV + v0), y = lds4(sV + j * PV + v0 + 4);
             const float2 v2[4] = {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)};
+            float kj[TK];
+            if constexpr (TK % 4 == 0) {
+#pragma unroll
+                for (int r = 0; r < TK; r += 4) {
+                    const float4 z = lds4(sK + j * PK + k0 + r);
+                    kj[r] = z.x; kj[r + 1] = z.y; kj[r + 2] = z.z; kj[r + 3] = z.w;
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < TK; ++r) kj[r] = sK[j * PK + k0 + r];
+            }
 #pragma unroll
             for (int r = 0; r < TK; ++r) {
-                const float2 kk = both(w * sK[j * PK + k0 + r]);
+                const float2 kk = both(w * kj[r]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) S[r][c] = fma2(kk, v2[c], S[r][c]);
             }
@@ -214,7 +245,7 @@ cudaError_t launch(const ScanArgs& a, cudaStream_t st) {
     const cudaError_t e = allow_smem<scan_simt_kernel<DKP, MODE>>((int)smem_bytes<DKP>());
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.seg_len ? a.slots : a.batch), a.H, (a.Dv + DVB - 1) / DVB);
-    scan_simt_kernel<DKP, MODE><<<grid, kThreads, smem_bytes<DKP>(), st>>>(a);
+    scan_simt_kernel<DKP, MODE><<<grid, threads<MODE>(), smem_bytes<DKP>(), st>>>(a);
     return cudaGetLastError();
 }
 
