@@ -199,7 +199,7 @@ template <typename T, int kRun, bool kBackward> constexpr int smem_bytes() {
 // rows, 32 / LPR rows to a warp.  Rows come through shared memory by asynchronous copies, each thread's
 // own kAhead rows deep: registers would hold too few loads in flight for HBM's latency.
 template <typename T, int kRun, int LPR, bool kInter, bool kBackward>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_rope_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) qk_norm_rope_kernel(Args a) {
     constexpr int RPW = 32 / LPR, RPB = RPW * kWarps, N = kRun;  // N packed pairs of values in a lane
     using Row = Raw<T, kRun>;
     extern __shared__ __align__(16) uint8_t ring[];
