@@ -356,11 +356,11 @@ ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* d, ssd_dtype dtyp
     {
         const Buffer ins[] = {row_buffer(q, rows, rs.q, H * Dk, es), row_buffer(k, rows, rs.k, Hk * Dk, es),
                               row_buffer(v, rows, rs.v, Hk * Dv, es), {log_decay, (uint64_t)H * 4},
-                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}, {workspace, need}};
-        const Buffer outs[] = {{o, (uint64_t)rows * H * Dv * es}, {final_state, state}};
+                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}};
+        const Buffer outs[] = {{o, (uint64_t)rows * H * Dv * es}, {final_state, state}, {workspace, need}};
         if (outputs_alias(outs, ins)) return SSD_ERR_UNSUPPORTED;
         if (init_state && init_state != final_state && overlap({init_state, state}, outs[1])) return SSD_ERR_UNSUPPORTED;
-        if (overlap({init_state, state}, outs[0])) return SSD_ERR_UNSUPPORTED;
+        if (overlap({init_state, state}, outs[0]) || overlap({init_state, state}, outs[2])) return SSD_ERR_UNSUPPORTED;
     }
     if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     if (d->batch == 0) return SSD_OK;
@@ -427,9 +427,9 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dty
     {
         const Buffer ins[] = {{q, n * H * Dk * es}, {k, n * Hk * Dk * es}, {v, n * Hk * Dv * es}, {d_o, n * H * Dv * es},
                               {init_state, state}, {d_final_state, state}, {log_decay, (uint64_t)H * 4},
-                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}, {workspace, need}};
+                              {cu_seqlens, ((uint64_t)d->batch + 1) * 8}};
         const Buffer outs[] = {{dq, n * H * Dk * es}, {dk, n * Hk * Dk * es}, {dv, n * Hk * Dv * es},
-                               {d_init_state, state}};
+                               {d_init_state, state}, {workspace, need}};
         if (outputs_alias(outs, ins)) return SSD_ERR_UNSUPPORTED;
     }
     if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_ERR_WORKSPACE;

@@ -494,10 +494,10 @@ ssd_status ssd_qk_norm_rope_backward(const ssd_qk_dims* d, ssd_dtype dtype, floa
     const struct { const void* p; uint64_t n; } in[] = {
         {q, T ? ((T - 1) * a.rs[0] + wq) * es : 0}, {k, T ? ((T - 1) * a.rs[1] + wk) * es : 0},
         {dq_out, T * wq * es}, {dk_out, T * wk * es}, {q_weight, nw}, {k_weight, nw}, {positions, T * 8},
-        {inv_freq, (uint64_t)d->rot_dim * 2}, {workspace, need}},
-        out[] = {{dq, T * wq * es}, {dk, T * wk * es}, {dq_weight, nw}, {dk_weight, nw}};
-    for (int i = 0; i < 4; ++i) {
-        for (int j = i + 1; j < 4; ++j)
+        {inv_freq, (uint64_t)d->rot_dim * 2}},
+        out[] = {{dq, T * wq * es}, {dk, T * wk * es}, {dq_weight, nw}, {dk_weight, nw}, {workspace, need}};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = i + 1; j < 5; ++j)
             if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return SSD_ERR_UNSUPPORTED;
         for (const auto& x : in)
             if (overlap(out[i].p, out[i].n, x.p, x.n)) return SSD_ERR_UNSUPPORTED;

@@ -263,6 +263,19 @@ def test_norm_rope_backward_refuses_overlaps_and_a_small_workspace(L):
     assert qk_backward_call(L, qk_dims(), ws=(vp(20), need - 1)) == WORKSPACE
 
 
+def test_a_workspace_over_an_input_is_refused(L):
+    """The kernels write it while others still read the inputs."""
+    d = la_dims(batch=1, nheads=4, seqlen=100000)
+    need = L.ssd_linear_attn_prefill_workspace_bytes(ctypes.byref(d), ops.SSD_BF16, 0)
+    assert need > 0
+    for i in range(5):  # log_decay, q, k, v, init_state
+        assert prefill_call(L, d, ws=(vp(i), need)) == UNSUPPORTED, i
+    for i in range(11):
+        assert backward_call(L, la_dims(), ws=(vp(i), 1 << 40)) == UNSUPPORTED, i
+    for i in range(12):
+        assert qk_backward_call(L, qk_dims(), ws=(vp(i), 1 << 30)) == UNSUPPORTED, i
+
+
 def test_binding_checks_tensors():
     t = torch.zeros(1, 4, 2, 64)
     with pytest.raises(ValueError):
