@@ -268,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, kBackward ? 2 : 3) qk_norm_rope_kern
             float2 ss = both(0.f);
 #pragma unroll
             for (int e = 0; e < N; ++e) ss = fma2(v[e], v[e], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_dim + a.eps);
+            const float mean2 = row_sum<LPR>(ss.x + ss.y) * inv_dim;  // by all lanes: it shuffles
+            const float r = row < rows ? rsqrtf(mean2 + a.eps) : 0.f;  // a place without a row stays zero where eps is
             if constexpr (!kBackward) {
 #pragma unroll
                 for (int e = 0; e < N; ++e) v[e] = mul2(mul2(v[e], both(r)), w[e]);

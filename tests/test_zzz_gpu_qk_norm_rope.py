@@ -172,3 +172,19 @@ def test_the_layer(dtype):
     w1, _, m1, _ = lo.prefill(qt[:, None], kt[:, None], vt[:, None], ld, D ** -0.5, S)
     assert (np.abs(np64(ot) - w1[:, 0]) <= n * m1[:, 0] + (U * np.abs(w1[:, 0]) if dtype == torch.bfloat16 else 0)).all()
     ops.device_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_without_an_epsilon(dtype):
+    """eps = 0 with rows that do not fill a block: the places without a row add nothing to the weights' gradients."""
+    x = make((5,), 3, 2, 64, 32, dtype, 12)
+    args = [x[n] for n in IN]
+    got = ops.qk_norm_rope_backward(x["dq_out"], x["dk_out"], *args, eps=0.0)
+    for n in "qk":
+        dx, dw, mx, mw = lo.norm_rope_grads(x[n], x[n + "_weight"], x["positions"], x["inv_freq"], 0.0, False,
+                                            x["d%s_out" % n])
+        big = np.max(mx, -1, keepdims=True)
+        assert (np.abs(np64(got[n]) - dx) <= bound(dx, 2 * big, dtype, 16 + 64)).all()
+        dy = np.max(np.abs(np64(x["d%s_out" % n])))
+        # 15 terms, each off by 16 roundings of the pair's larger channel (|x r| <= sqrt(64) = 8)
+        assert (np.abs(np64(got[n + "_weight"]) - dw) <= 32 * E * (mw + 15 * 8 * 2 * dy)).all()
