@@ -140,6 +140,7 @@ template <typename T> __global__ void __launch_bounds__(256) group_sum_kernel(Gr
     if (i >= g.quads) return;
     const int per = g.width / 4;
     const int64_t head = i / per;  // (row, head) of dst
+    if (a.cu && ((uint64_t)head < (uint64_t)a.cu[0] * a.heads || (uint64_t)head >= (uint64_t)a.cu[a.batch] * a.heads)) return;
     const float* p = g.src + (head * a.group * per + (i - head * per)) * 4;
     float4 t = load4(p);
     for (int k = 1; k < a.group; ++k) {
@@ -167,12 +168,12 @@ cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_group_sums(GroupSums a, int64_t rows, int heads, bool bf16, cudaStream_t st) {
+cudaError_t launch_group_sums(GroupSums a, int64_t rows, bool bf16, cudaStream_t st) {
     int64_t blocks = 0;
     for (GroupSum& g : a.sum) {
-        g.quads = rows * heads * (g.width / 4);
+        g.quads = rows * a.heads * (g.width / 4);
         g.blocks = (unsigned)((g.quads + 255) / 256);
-        blocks += g.blocks;
+        blocks += (g.quads + 255) / 256;
     }
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
@@ -500,7 +501,9 @@ ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* d, ssd_dtype dty
         e = launch_scans(a, 3, kWhole, cs);
     }
     if (e == cudaSuccess && group > 1)
-        e = launch_group_sums(GroupSums{{{dk_heads, dk, (int)Dk}, {dv_heads, dv, (int)Dv}}, group}, rows, (int)Hk, base.bf16, cs);
+        e = launch_group_sums(
+            GroupSums{{{dk_heads, dk, (int)Dk}, {dv_heads, dv, (int)Dv}}, group, (int)Hk, cu_seqlens, d->batch}, rows,
+            base.bf16, cs);
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

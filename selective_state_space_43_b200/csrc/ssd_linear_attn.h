@@ -109,7 +109,8 @@ cudaError_t launch_scan_tc(const ScanArgs* scans, int count, Mode mode, cudaStre
 // One or two scans of a call in one launch.
 cudaError_t launch_combine(const ScanArgs* scans, int count, cudaStream_t st);
 // dst[row][head][:] = sum over the `group` scan heads that share the head of src[row][head * group + g][:]; two
-// such sums (of keys and of values) in one launch.
+// such sums (of keys and of values) in one launch.  Rows outside every packed sequence, whose src nobody wrote, are left
+// out.
 struct GroupSum {
     const float* src;
     void* dst;
@@ -119,9 +120,11 @@ struct GroupSum {
 };
 struct GroupSums {
     GroupSum sum[2];
-    int group;
+    int group, heads;         // scan heads to a head of dst; heads of dst
+    const int64_t* cu;        // offsets of packed sequences or nullptr
+    int64_t batch;
 };
-cudaError_t launch_group_sums(GroupSums a, int64_t rows, int heads, bool bf16, cudaStream_t st);
+cudaError_t launch_group_sums(GroupSums a, int64_t rows, bool bf16, cudaStream_t st);
 
 struct DecodeArgs {
     int64_t batch;

@@ -427,3 +427,28 @@ def test_a_lone_chunk_rounds_its_outputs_only(L, H, dk, dv):
     o, _ = ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"])
     wo, _, mo, _ = lo.prefill(x["q"], x["k"], x["v"], x["log_decay"], dk ** -0.5)
     assert (np.abs(np64(o) - wo) <= U * np.abs(wo) * 1.001 + (2.0 ** -15 + n_terms(L, dk) * E) * mo).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("Hk", [1, 2])
+@pytest.mark.parametrize("rows,cu", [(300, [7, 100, 263]), (4000, [5, 261, 2821, 3077]), (40, [9, 9]), (10, [10, 10])])
+def test_gradients_outside_every_sequence_are_left_as_they_were(rows, cu, Hk, dtype):
+    """The caller's dq, dk, dv through the C entry point, with heads of their own and shared ones (whose gradients are
+    summed by a kernel of its own)."""
+    import ctypes
+    H, dk, dv, n = 2, 64, 40, len(cu) - 1
+    x = make(rows, (rows,), H, Hk, dk, dv, dtype, nseq=n, grads=True)
+    offsets = torch.tensor(cu).cuda()
+    # the same call: a gradient of the initial state that nobody asks for leaves V' in fewer parts
+    want = ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], cu_seqlens=offsets,
+                                    want_init_grads=False)
+    got = {name: torch.full_like(x[name], 7.0) for name in "qkv"}
+    ws = torch.full((workspace_bytes(rows, H, Hk, dk, dv, dtype, True, n, True) + 16,), 3, dtype=torch.uint8, device="cuda")
+    ops._enqueue("ssd_linear_attn_backward", x["q"].device, ctypes.byref(ops.SsdLinearAttnDims(n, rows, H, Hk, dk, dv)),
+                 1 if dtype == torch.bfloat16 else 0, x["log_decay"].data_ptr(), dk ** -0.5, offsets.data_ptr(),
+                 x["q"].data_ptr(), x["k"].data_ptr(), x["v"].data_ptr(), None, x["do"].data_ptr(), None,
+                 got["q"].data_ptr(), got["k"].data_ptr(), got["v"].data_ptr(), None, ws.data_ptr(), ws.numel())
+    ops.device_status()
+    for name in "qkv":
+        assert torch.equal(got[name][cu[0]:cu[-1]], want[name][cu[0]:cu[-1]]), name
+        assert (got[name][:cu[0]] == 7).all() and (got[name][cu[-1]:] == 7).all(), name
