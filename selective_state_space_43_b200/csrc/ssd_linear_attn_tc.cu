@@ -76,7 +76,7 @@ struct Params {
 };
 
 // Moves registers between warpgroups.  Launched with 896 x 72; with outputs 256 x 112 (scores) + 256 x 40 (V') + 256 x 80
-// (S and outputs) + 128 x 40, without them 256 x 40 + 256 x 64 + 256 x 104 + 128 x 56: never more than launched.
+// (S and outputs) + 128 x 40, without them 256 x 40 + 256 x 64 + 256 x 104 + 128 x 72: never more than launched.
 template <int N> __device__ __forceinline__ void regs_more() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };
 
     if (warp >= kWarpTma) {
-        regs_fewer<kOut ? 40 : 56>();
+        if constexpr (kOut) regs_fewer<40>();
         if (warp == kWarpItem) {
             // ---- items ----
             const ScanArgs& call = prm.scan[0].a;  // a launch's scans have the same sequences
@@ -361,42 +361,52 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 end.scan = -1;
                 if (!announce(end)) *stop = 1;
             }
-        } else if (warp == kWarpTma && lane == 0) {
-            // ---- tile loads ----
+        } else if (warp == kWarpTma) {
+            // ---- tile loads.  The whole warp runs this loop, so that addresses stay in uniform registers; one elected lane
+            // issues.
             Ring ring;
             const Item* it;
             // a place's products are complete (at once where there were none)
-            auto freed = [&](int bar, int i) { return mbar_wait(&bars[bar + i], ((ring.phases >> i) & 1) ^ 1, stop); };
-            for (int k = 0; !*stop && (it = enter(k, false)) != nullptr; ++k) {
-                const Scan& scan = prm.scan[it->scan];
+            auto freed = [&](int bar, int i) { return warp_wait(&bars[bar + i], ((ring.phases >> i) & 1) ^ 1, stop); };
+            bool ok = true;
+            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+                const Scan& scan = prm.scan[__shfl_sync(0xffffffffu, it->scan, 0)];
                 const ScanArgs& a = scan.a;
-                const int h = it->h, dv0 = it->dv0, nc = it->nc, row0 = it->row0;
+                const int dv0 = __shfl_sync(0xffffffffu, it->dv0, 0), nc = __shfl_sync(0xffffffffu, it->nc, 0);
+                const int row0 = __shfl_sync(0xffffffffu, it->row0, 0), h = __shfl_sync(0xffffffffu, it->h, 0);
+                const int hk = h / a.gk, hv = h / a.gv, hq = kOut ? h / a.gq : 0;
                 const bool rev = a.reverse;
-                leave(k, false);
-                bool ok = true;
+                leave(k, true);
                 if (ring.cut(a.Dk, kOut))
                     for (int i = 0; i < kStages; ++i)
                         ok = ok && freed(KFREE, i) && (!kOut || freed(QFREE, i)) && freed(VFREE, i);
-                if (nc == 0) mbar_arrive(&bars[LASTLOAD]);
+                if (nc == 0 && elect_one()) mbar_arrive(&bars[LASTLOAD]);
                 for (int c = 0; ok && c < nc; ++c) {
-                    if (c == max(0, nc - 3)) mbar_arrive(&bars[LASTLOAD]);
                     const int s = ring.s, r = row0 + place_of(rev, nc, c) * C;
                     ok = freed(KFREE, s);
-                    mbar_arrive_expect_tx(&bars[FULL + s], (ring.kb + 1 + (kOut ? ring.kb : 0)) * kBox);
                     // each tile as soon as its place is free (and in any case: the bytes are expected)
-                    for (int b = 0; b < ring.kb; ++b)
-                        tma_load_3d(sm + ring.k(kOut) + b * kBox, &scan.tk, &bars[FULL + s], b * 64, h / a.gk, r);
+                    if (elect_one()) {
+                        if (c == max(0, nc - 3)) mbar_arrive(&bars[LASTLOAD]);
+                        mbar_arrive_expect_tx(&bars[FULL + s], (ring.kb + 1 + (kOut ? ring.kb : 0)) * kBox);
+                        tma_load_3d(sm + ring.k(kOut), &scan.tk, &bars[FULL + s], 0, hk, r);
+                        if (ring.kb == 2) tma_load_3d(sm + ring.k(kOut) + kBox, &scan.tk, &bars[FULL + s], 64, hk, r);
+                    }
+                    __syncwarp();
                     if (kOut) {
                         ok = ok && freed(QFREE, s);
-                        for (int b = 0; b < ring.kb; ++b)
-                            tma_load_3d(sm + ring.q(kOut) + b * kBox, &scan.tq, &bars[FULL + s], b * 64, h / a.gq, r);
+                        if (elect_one()) {
+                            tma_load_3d(sm + ring.q(kOut), &scan.tq, &bars[FULL + s], 0, hq, r);
+                            if (ring.kb == 2) tma_load_3d(sm + ring.q(kOut) + kBox, &scan.tq, &bars[FULL + s], 64, hq, r);
+                        }
+                        __syncwarp();
                     }
                     ok = ok && freed(VFREE, s);
-                    tma_load_3d(sm + ring.v(kOut), &scan.tv, &bars[FULL + s], dv0, h / a.gv, r);
+                    if (elect_one()) tma_load_3d(sm + ring.v(kOut), &scan.tv, &bars[FULL + s], dv0, hv, r);
+                    __syncwarp();
                     ring.step();
                 }
-                if (!ok) *stop = 1;
             }
+            if (!ok) *stop = 1;
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
             for (int i = 0; i < kStages; ++i) mbar_wait(&bars[FULL + i], ((ring.phases >> i) & 1) ^ 1, nullptr, 100000000ull);
         } else if (warp == kWarpMma) {
