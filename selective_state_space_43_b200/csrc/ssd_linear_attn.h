@@ -70,8 +70,12 @@ __device__ inline Span sequence_span(const ScanArgs& a, int64_t b) {
     if (r0 < 0 || r1 < r0 || r1 > a.rows) return Span{0, 0, false};
     return Span{r0, r1 - r0, true};
 }
+// Segments of a sequence that is not packed: 32-bit arithmetic (rows < 2^31), for this is on the way to a block's first load.
+__device__ inline uint32_t segments_each(const ScanArgs& a) {
+    return ((uint32_t)a.L + (uint32_t)a.seg_len - 1) / (uint32_t)a.seg_len;
+}
 __device__ inline int64_t first_slot(const ScanArgs& a, int64_t b, const Span& s) {
-    return a.cu ? s.start / a.seg_len + b : b * ((a.L + a.seg_len - 1) / a.seg_len);
+    return a.cu ? s.start / a.seg_len + b : b * segments_each(a);
 }
 __device__ inline Segment segment_of(const ScanArgs& a, int64_t slot) {
     if (a.seg_len == 0) {
@@ -88,7 +92,7 @@ __device__ inline Segment segment_of(const ScanArgs& a, int64_t slot) {
         }
         b = lo;
     } else {
-        b = slot / ((a.L + a.seg_len - 1) / a.seg_len);
+        b = (uint32_t)slot / segments_each(a);
     }
     const Span s = sequence_span(a, b);
     const int64_t i = slot - first_slot(a, b, s), r = i * a.seg_len;

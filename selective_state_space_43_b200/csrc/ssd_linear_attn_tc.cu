@@ -24,7 +24,8 @@
 // 28 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
 //   8-15  V' (shared memory -> shared memory), 32 channels each; the same threads zero the rows behind a sequence's end
-//         in K and V
+//         in K and V.  Where states alone are wanted there are no scores, so 0-15 make V', 16 channels each, and it has two
+//         places, so that the next is made while the product reads the last (one prompt of 8191 rows: 78 -> 76 us)
 //   16-23 S: TMEM -> registers -> shared memory, and o: TMEM -> registers -> global, a row per thread in 32-byte stores;
 //         32 channels each
 //   24    TMA: K, V, Q of a chunk, two or three stages
@@ -51,6 +52,8 @@ constexpr int kRegisters = 72;  // of a thread at launch
 constexpr uint32_t kBox = 16384;                 // 128 rows of 128 bytes
 constexpr uint32_t OFF_VP = 10 * kBox;           // behind the stages; V': up to three boxes
 constexpr uint32_t OFF_S = OFF_VP + 3 * kBox;    // bf16 copy of S, [128 key rows][64 channels]
+// Without outputs the stages end at 9 boxes and there is no copy of S: two places of two boxes for V', one of its third part.
+constexpr uint32_t OFF_VP2 = 9 * kBox, OFF_V3 = OFF_S;
 constexpr uint32_t OFF_BAR = OFF_S + kBox;
 constexpr uint32_t OFF_STOP = OFF_BAR + 256, OFF_TMEM = OFF_BAR + 264, OFF_ANSWER = OFF_BAR + 272, OFF_ITEM = OFF_BAR + 288;
 constexpr uint32_t OFF_ORDER = OFF_BAR + 512;
@@ -76,7 +79,7 @@ struct Params {
 };
 
 // Moves registers between warpgroups.  Launched with 896 x 72; with outputs 256 x 112 (scores) + 256 x 40 (V') + 256 x 80
-// (S and outputs) + 128 x 40, without them 256 x 40 + 256 x 64 + 256 x 104 + 128 x 72: never more than launched.
+// (S and outputs) + 128 x 40, without them 512 x 64 (V') + 256 x 88 + 128 x 72: never more than launched.
 template <int N> __device__ __forceinline__ void regs_more() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
@@ -244,13 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
     constexpr bool kOut = kMode != kStates;
     constexpr int kMaxParts = kMode == kOutputs ? 2 : 3;  // of V'
+    constexpr int kVWarps = kOut ? 8 : 16;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], i == PREADY || i == VREADY || i == SREADY || i == EPI || i == DSREAD || i == DSREAD + 1 ? 8
-                                    : i >= IEMPTY ? (kOut ? 26 : 18)  // warps that read an item
+                mbar_init(&bars[i], i == VREADY ? kVWarps
+                                    : i == PREADY || i == SREADY || i == EPI || i == DSREAD || i == DSREAD + 1 ? 8
+                                    : i >= IEMPTY ? 26  // warps that read an item
                                                   : 1);
             *stop = 0;
             fence_mbar_init();
@@ -374,10 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 const ScanArgs& a = scan.a;
                 const int dv0 = __shfl_sync(0xffffffffu, it->dv0, 0), nc = __shfl_sync(0xffffffffu, it->nc, 0);
                 const int row0 = __shfl_sync(0xffffffffu, it->row0, 0), h = __shfl_sync(0xffffffffu, it->h, 0);
-                const int hk = h / a.gk, hv = h / a.gv, hq = kOut ? h / a.gq : 0;
+                auto stored = [&](int group) { return group == 1 ? h : h / group; };  // the stored head of a role
+                const int hk = stored(a.gk), hv = a.gv == a.gk ? hk : stored(a.gv), hq = kOut ? stored(a.gq) : 0;
                 const bool rev = a.reverse;
                 leave(k, true);
-                if (ring.cut(a.Dk, kOut))
+                if (ring.cut(a.Dk, kOut) && k > 0)
                     for (int i = 0; i < kStages; ++i)
                         ok = ok && freed(KFREE, i) && (!kOut || freed(QFREE, i)) && freed(VFREE, i);
                 if (nc == 0 && elect_one()) mbar_arrive(&bars[LASTLOAD]);
@@ -450,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                          (kOut || cc < 2 || warp_wait(&bars[DSREAD + (cc & 1)], ((cc >> 1) - 1) & 1, stop));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t dKt = sw128_desc(tk, 16384, 1024), dVP = sw128_desc(base + OFF_VP, 16384, 1024);
+                    const uint64_t dKt = sw128_desc(tk, 16384, 1024), dVP = sw128_desc(base + (kOut ? OFF_VP : OFF_VP2 + (cc & 1) * 2 * kBox), 16384, 1024);
+                    const uint64_t dV3 = kOut ? dVP + 16 * 128 : sw128_desc(base + OFF_V3, 16384, 1024);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -458,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (kMaxParts == 3 && nc - c <= third) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                mma_bf16(ds + 64, dKt + k * 128, dVP + (16 + k) * 128, ID_DS3, 1);
+                                mma_bf16(ds + 64, dKt + k * 128, dV3 + k * 128, ID_DS3, 1);
                         }
                         mma_commit(&bars[DSFULL + (cc & 1)]);
                         mma_commit(&bars[KFREE + s]);
@@ -504,10 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             __syncwarp();
             mbar_wait(&bars[MMADONE], 0, nullptr, 100000000ull);
         }
-    } else if (warp < 8) {
-        if (!kOut) {
-            regs_fewer<40>();
-        } else {
+    } else if (kOut && warp < 8) {
+        if constexpr (kOut) {
             regs_more<112>();
             // ---- scores: row `row`, columns 64 half .. 64 half + 63 ----
             const int j0 = (warp >> 2) * 64;
@@ -582,9 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             if (!ok) *stop = 1;
         }
     } else if (warp < kWarpOut) {
-        // ---- V': tile row `row`, 32 of the 64 channels ----
+        // ---- V': tile row `row`, 64 * 4 / kVWarps of the 64 channels ----
         regs_fewer<kOut ? 40 : 64>();
-        const int half = (warp >> 2) & 1;
+        constexpr int kPieces = 32 / kVWarps;  // of 8 channels
+        const int share = (warp >> 2) & (kVWarps / 4 - 1);
         int cc = 0;
         Ring ring;
         const Item* it;
@@ -611,16 +617,18 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t o = sw128_off(row, i);
                         const uint4 z = make_uint4(0, 0, 0, 0);
-                        if (half < ring.kb) *reinterpret_cast<uint4*>(sm + ring.k(kOut) + half * kBox + o) = z;
-                        if (i / 4 == half) *reinterpret_cast<uint4*>(tv + o) = z;
+                        if (share < ring.kb) *reinterpret_cast<uint4*>(sm + ring.k(kOut) + share * kBox + o) = z;
+                        if (i / kPieces == share) *reinterpret_cast<uint4*>(tv + o) = z;
                     }
                 }
-                // the product that reads the last V' is complete
-                ok = cc == 0 || warp_wait(&bars[DSFULL + ((cc - 1) & 1)], ((cc - 1) >> 1) & 1, stop);
-                if (!ok) break;
-#pragma unroll 2
-                for (int i = 0; i < kHalf / 8; ++i) {
-                    const uint32_t o = sw128_off(row, half * 4 + i);
+                // the product that reads the V' in this place is complete
+                auto multiplied = [&](int chunk) {
+                    return chunk < 0 || warp_wait(&bars[DSFULL + (chunk & 1)], (chunk >> 1) & 1, stop);
+                };
+                if (!(ok = multiplied(kOut ? cc - 1 : cc - 2))) break;
+                uint8_t* vp = sm + (kOut ? OFF_VP : OFF_VP2 + (cc & 1) * 2 * kBox);
+                auto piece = [&](int i, auto write) {  // 8 channels of V', cut into parts
+                    const uint32_t o = sw128_off(row, share * kPieces + i);
                     const uint4 x = *reinterpret_cast<const uint4*>(tv + o);
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t part[kMaxParts][4];
@@ -637,9 +645,20 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     }
 #pragma unroll
                     for (int t = 0; t < kMaxParts; ++t)
-                        if (t < 2 || three)
-                            *reinterpret_cast<uint4*>(sm + OFF_VP + t * kBox + o) =
-                                make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
+                        write(t, o, make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]));
+                };
+#pragma unroll 2
+                for (int i = 0; i < kPieces; ++i)
+                    piece(i, [&](int t, uint32_t o, uint4 p) {
+                        if (t < 2 || (kOut && three)) *reinterpret_cast<uint4*>(vp + t * kBox + o) = p;
+                    });
+                if (!kOut && three) {  // the third part has one place, so it is made (anew) when that is free
+                    if (!(ok = multiplied(cc - 1))) break;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        piece(i, [&](int t, uint32_t o, uint4 p) {
+                            if (t == 2) *reinterpret_cast<uint4*>(sm + OFF_V3 + o) = p;
+                        });
                 }
                 fence_async_smem();
                 warp_arrive(&bars[VREADY], lane);
@@ -648,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (!ok) *stop = 1;
     } else {
         // ---- S: key row `row`, and the outputs: tile row `row`; 32 of the 64 channels ----
-        regs_more<kOut ? 80 : 104>();
+        regs_more<kOut ? 80 : 88>();
         const int half = (warp >> 2) & 1;
         float S[kHalf];
         int cc = 0;
