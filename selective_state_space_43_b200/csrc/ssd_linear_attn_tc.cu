@@ -60,6 +60,8 @@ constexpr uint32_t OFF_ORDER = OFF_BAR + 512;
 constexpr int kSorted = 64;   // packed sequences that are taken longest first
 constexpr uint32_t kSmemBytes = OFF_ORDER + kSorted + 1024;  // + alignment of the base
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
+// PREADY: without outputs, where there are no scores, V' is ready in its second place (VREADY: in its first).  One barrier for
+// both would be completed twice before the products' warp looks, and take a fast warp's arrival for a slow one's.
 constexpr int kStages = 3;  // at most
 enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, DSFULL = 12, DSREAD = 14, PFULL = 16, PREADY, VREADY, SREADY, Y2DONE, YFULL,
            EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     if (warp == kWarpMma) {
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
-                mbar_init(&bars[i], i == VREADY ? kVWarps
+                mbar_init(&bars[i], i == VREADY || (!kOut && i == PREADY) ? kVWarps
                                     : i == PREADY || i == SREADY || i == EPI || i == DSREAD || i == DSREAD + 1 ? 8
                                     : i >= IEMPTY ? 26  // warps that read an item
                                                   : 1);
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     // dS = K^T V' (its buffer was read before the S that the last Y2 waited for, if there is one): the parts lie one box
                     // behind the other, the first two are one product with 64 columns each, so that K is read once; the
                     // third adds to the second
-                    ok = warp_wait(&bars[VREADY], cc & 1, stop) &&
+                    ok = warp_wait(&bars[kOut || !(cc & 1) ? VREADY : PREADY], (kOut ? cc : cc >> 1) & 1, stop) &&
                          (kOut || cc < 2 || warp_wait(&bars[DSREAD + (cc & 1)], ((cc >> 1) - 1) & 1, stop));
                     if (!ok) break;
                     tc_fence_after();
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         });
                 }
                 fence_async_smem();
-                warp_arrive(&bars[VREADY], lane);
+                warp_arrive(&bars[kOut || !(cc & 1) ? VREADY : PREADY], lane);
             }
         }
         if (!ok) *stop = 1;

@@ -452,3 +452,19 @@ def test_gradients_outside_every_sequence_are_left_as_they_were(rows, cu, Hk, dt
     for name in "qkv":
         assert torch.equal(got[name][cu[0]:cu[-1]], want[name][cu[0]:cu[-1]]), name
         assert (got[name][:cu[0]] == 7).all() and (got[name][cu[-1]:] == 7).all(), name
+
+
+@pytest.mark.parametrize("B,L,H,dk,dv", [(1, 8191, 16, 128, 128), (1, 6000, 20, 64, 64), (3, 2500, 8, 128, 64)])
+def test_segments_give_the_same_bits_over_many_runs(B, L, H, dk, dv):
+    """The warps of the states' pass run up to two chunks apart: none may be taken for another's."""
+    assert workspace_bytes(L, H, H, dk, dv, torch.bfloat16, B=B) > 0
+    x = make(L, (B, L), H, H, dk, dv, torch.bfloat16, grads=True)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, S = ops.linear_attn_prefill(*args)
+    g = ops.linear_attn_backward(*args, x["do"])
+    ops.device_status()
+    for _ in range(100):
+        o2, S2 = ops.linear_attn_prefill(*args)
+        g2 = ops.linear_attn_backward(*args, x["do"])
+        assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(g[n], g2[n]) for n in g)
+    ops.device_status()
