@@ -26,8 +26,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 // ---- one token ----------------------------------------------------------------------------------------------
 // S <- e^l S + k v^T, o = scale q S: every state element is read once and written once, two FMAs each, so the
-// step is bound by HBM.  One block per (sequence, head); a thread holds four value channels and walks the key
-// rows with eight 16-byte loads in flight; the rows' partial outputs are joined in shared memory in a fixed order.
+// step is bound by HBM (256 sequences of 128 heads 128 x 64: 355 us, 6.1 TB/s).  One block per (sequence, head); a thread
+// holds four value channels and walks the key rows with eight 16-byte loads in flight; the rows' partial outputs are joined in shared memory in a fixed order.
 constexpr int kDecThreads = 256, kDecRows = 8;
 
 template <typename T>
@@ -246,10 +246,10 @@ cudaError_t launch_scans(const ScanArgs* scans, int count, Mode mode, cudaStream
 // costs `start`, and per row `row` for outputs and state or `state_row` for states alone; blocks run `slots` at a
 // time in each of a pass's launches; the cut adds two launches (`extra`) and the writing, joining and reading of its
 // states at `state_rate` bytes a microsecond.  Both sides of the rule as measured (B200, whole sequences against the
-// chosen cut): bf16, 1 x 8191 rows, 16 heads of 128 x 128: 143 against 89 us (2048 rows; 126 to 140 us at 1024 and
-// 4096); 4 x 8192 rows, 64 heads of 128 x 64: 324 us whole (579 at 4096 rows).  fp32, 1 x 256 rows, 4 heads of 32 x 64:
-// 42 against 17 us (32 rows); 2 x 2048 rows, 8 heads of 128 x 128: 760 against 193 us (256 rows); 16 x 300 rows, 8
-// heads of 96 x 64: 103 us whole (126 at 128 rows).
+// chosen cut): bf16, 1 x 8191 rows, 16 heads of 128 x 128: 138 against 72 us (2048 rows; 90 at 512); 4 x 8192 rows, 64
+// heads of 128 x 64: 294 us whole (450 at 2048 rows).  fp32, 1 x 256 rows, 4 heads of 32 x 64: 31 against 14 us (32
+// rows); 2 x 2048 rows, 8 heads of 128 x 128: 544 against 175 us (256 rows); 16 x 300 rows, 8 heads of 96 x 64: 74 us
+// whole (120 at 128 rows); 4 x 1000 rows, 32 heads of 128 x 128: 438 us whole (712 at 256 rows).
 struct Cost {
     double start, row, state_row, extra, state_rate, slots;
     int64_t least;  // rows of a segment: a chunk of the kernel

@@ -31,8 +31,10 @@
 //   24    TMA: K, V, Q of a chunk, two or three stages
 //   25    tcgen05.mma
 //   26    the CTA's items (27 only completes the warpgroup)
-// Bound by HBM where there are enough heads: Q, K, V are read once (Q and K once for each 64 value
-// channels, the second time from L2), o written once.
+// Q, K, V are read once (Q and K once for each 64 value channels, the second time from L2), o written once.  Where heads
+// are many the power limit bounds it: 2 x 8192 rows of 74 heads 128 x 64 take 195 us (4.8 TB/s) at the 1365 MHz that it
+// leaves, and 152 us (6.1 TB/s) on zeros, which draw less, at 1965 MHz; 4 x 8192 rows of 64 heads 354 us.  Where they are
+// few, the chain scores - mask - products - outputs of a chunk does: one prompt of 8191 rows, 16 heads 128 x 128, 75 us.
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 #include "ssd_linear_attn.h"
@@ -458,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                          (kOut || cc < 2 || warp_wait(&bars[DSREAD + (cc & 1)], ((cc >> 1) - 1) & 1, stop));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t dKt = sw128_desc(tk, 16384, 1024), dVP = sw128_desc(base + (kOut ? OFF_VP : OFF_VP2 + (cc & 1) * 2 * kBox), 16384, 1024);
+                    const uint64_t dKt = sw128_desc(tk, 16384, 1024);
+                    const uint64_t dVP = sw128_desc(base + (kOut ? OFF_VP : OFF_VP2 + (cc & 1) * 2 * kBox), 16384, 1024);
                     const uint64_t dV3 = kOut ? dVP + 16 * 128 : sw128_desc(base + OFF_V3, 16384, 1024);
                     if (elect_one()) {
 #pragma unroll
