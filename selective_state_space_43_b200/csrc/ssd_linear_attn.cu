@@ -27,7 +27,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // ---- one token ----------------------------------------------------------------------------------------------
 // S <- e^l S + k v^T, o = scale q S: every state element is read once and written once, two FMAs each, so the
 // step is bound by HBM (256 sequences of 128 heads 128 x 64: 355 us, 6.1 TB/s).  One block per (sequence, head); a thread
-// holds four value channels and walks the key rows with eight 16-byte loads in flight; the rows' partial outputs are joined in shared memory in a fixed order.
+// holds four value channels and walks the key rows with eight 16-byte loads in flight; the rows' partial outputs are
+// joined in shared memory in a fixed order.
 constexpr int kDecThreads = 256, kDecRows = 8;
 
 template <typename T>

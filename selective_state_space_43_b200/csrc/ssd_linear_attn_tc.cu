@@ -16,10 +16,10 @@
 // accumulator is carried through the tensor cores, and nothing but those warps' multiply-adds depends on the
 // chunk before.
 //
-// Roundings: scores (times their decay) to bf16, the A operand of Y1 (in a sequence of one chunk to two bf16 parts); the
-// copy of S that Y2 reads to bf16 (S itself stays fp32); o once.  V' is cut into bf16 parts of 8 bits (v w = hi + mid +
-// lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits) where what the second leaves would show in a
-// state that the caller gets, so that such a state is as exact as fp32 sums.
+// Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself stays
+// fp32); both to two bf16 parts in a sequence of one chunk, whose few outputs may share their errors; o once.  V' is cut
+// into bf16 parts of 8 bits (v w = hi + mid + lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits)
+// where what the second leaves would show in a state that the caller gets, so that such a state is as exact as fp32 sums.
 //
 // 28 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
@@ -290,6 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     };
     // Whether the scores are kept in two bf16 parts: a lone chunk may have few outputs, which all share a score's error.
     auto two_parts = [](int nc) { return nc == 1; };
+    // Whether the same holds for the state that its outputs start from: the copy of S is then written twice, what the first
+    // leaves after the product with the first.
+    auto two_copies = [&](const ScanArgs& a, int nc) { return kMode == kWhole && two_parts(nc) && a.init; };
     // the place of chunk c, in scan order, among the item's chunks; the rows of the chunk at a place
     auto place_of = [](bool rev, int nc, int c) { return rev ? nc - 1 - c : c; };
     auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };
@@ -427,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             constexpr uint32_t ID_DS = idesc_bf16_f32(128, 128, true, true), ID_DS3 = idesc_bf16_f32(128, 64, true, true);
             uint32_t base = smem_u32(sm);
             int cc = 0;  // the CTA's chunks over all its items
+            int sc = 0;  // copies of S
             Ring ring;
             const Item* it;
             bool ok = true;
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 ring.cut(prm.scan[it->scan].a.Dk, kOut);
                 const bool wide = ring.kb == 2;
                 const int nc = it->nc, third = it->third;
+                const bool twice = two_copies(prm.scan[it->scan].a, nc);
                 leave(k, true);
                 for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
                     const int s = ring.s;
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     __syncwarp();
                     if (kOut) {
                         // Y2 = Q S, once S is written and the outputs before have been read
-                        ok = warp_wait(&bars[SREADY], cc & 1, stop) && (cc == 0 || warp_wait(&bars[EPI], (cc - 1) & 1, stop));
+                        ok = warp_wait(&bars[SREADY], sc & 1, stop) && (cc == 0 || warp_wait(&bars[EPI], (cc - 1) & 1, stop));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t dS = sw128_desc(base + OFF_S, 16384, 1024);
@@ -486,9 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 0);
                             if (wide) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
                             mma_commit(&bars[Y2DONE]);
-                            mma_commit(&bars[QFREE + s]);
+                            if (!twice) mma_commit(&bars[QFREE + s]);
                         }
                         __syncwarp();
+                        ++sc;
                         // Y1 = P V
                         if (!(ok = warp_wait(&bars[PREADY], cc & 1, stop))) break;
                         tc_fence_after();
@@ -502,9 +508,22 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                 for (int k = 0; k < 8; ++k)
                                     mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + k * 16 + 8, dV + k * 128, ID_Y, 1);
                             }
-                            mma_commit(&bars[YFULL]);
+                            if (!twice) mma_commit(&bars[YFULL]);
                         }
                         __syncwarp();
+                        if (twice) {  // Y2 += Q (what the first copy left of S)
+                            if (!(ok = warp_wait(&bars[SREADY], sc & 1, stop))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                mma_k64<true>(tmem + COL_Y2, dQ, dS, ID_Y, 1);
+                                if (wide) mma_k64<true>(tmem + COL_Y2, dQ + (kBox >> 4), dS + 4 * 128, ID_Y, 1);
+                                mma_commit(&bars[Y2DONE]);
+                                mma_commit(&bars[QFREE + s]);
+                                mma_commit(&bars[YFULL]);
+                            }
+                            __syncwarp();
+                            ++sc;
+                        }
                     }
                     if (elect_one()) mma_commit(&bars[VFREE + s]);
                     __syncwarp();
@@ -675,18 +694,28 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         regs_more<kOut ? 80 : 88>();
         const int half = (warp >> 2) & 1;
         float S[kHalf];
-        int cc = 0;
+        int cc = 0, sc = 0;  // chunks, copies of S
         const Item* it;
         bool ok = true;
-        auto publish = [&] {  // the bf16 copy that Y2 reads
+        auto publish = [&](bool rest) {  // the bf16 copy that Y2 reads, or what it leaves of S
+            // over the copy before, once the product has read it
+            ok = sc == 0 || warp_wait(&bars[Y2DONE], (sc - 1) & 1, stop);
+            if (!ok) return;
             uint8_t* p = sm + OFF_S;
 #pragma unroll
-            for (int i = 0; i < kHalf / 8; ++i)
-                *reinterpret_cast<uint4*>(p + sw128_off(row, half * 4 + i)) =
-                    make_uint4(pack_bf2(S[8 * i], S[8 * i + 1]), pack_bf2(S[8 * i + 2], S[8 * i + 3]),
-                               pack_bf2(S[8 * i + 4], S[8 * i + 5]), pack_bf2(S[8 * i + 6], S[8 * i + 7]));
+            for (int i = 0; i < kHalf / 8; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = S[8 * i + 2 * j], y = S[8 * i + 2 * j + 1];
+                    w[j] = pack_bf2(x, y);
+                    if (rest) w[j] = pack_bf2(x - bf_lo(w[j]), y - bf_hi(w[j]));
+                }
+                *reinterpret_cast<uint4*>(p + sw128_off(row, half * 4 + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
             fence_async_smem();
             warp_arrive(&bars[SREADY], lane);
+            ++sc;
         };
         // the item is read from its place in the ring wherever it is needed, not kept in registers
         for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
@@ -722,10 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                             }
                     }
                 }
-                if (it->nc > 0) {  // over the S that the item before left, once it has been read
-                    ok = cc == 0 || warp_wait(&bars[Y2DONE], (cc - 1) & 1, stop);
-                    if (ok) publish();
-                }
+                if (it->nc > 0) publish(false);
+                if (ok && two_copies(a, it->nc)) publish(true);
             }
             for (int c = 0; ok && c < it->nc; ++c, ++cc) {
                 if (!(ok = warp_wait(&bars[DSFULL + (cc & 1)], (cc >> 1) & 1, stop))) break;
@@ -752,8 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     warp_arrive(&bars[DSREAD + (cc & 1)], lane);
                 } else {
                     if (c + 1 < it->nc) {
-                        if (!(ok = warp_wait(&bars[Y2DONE], cc & 1, stop))) break;
-                        publish();
+                        publish(false);
+                        if (!ok) break;
                     }
                     if (!(ok = warp_wait(&bars[YFULL], cc & 1, stop))) break;
                     tc_fence_after();

@@ -468,3 +468,46 @@ def test_segments_give_the_same_bits_over_many_runs(B, L, H, dk, dv):
         g2 = ops.linear_attn_backward(*args, x["do"])
         assert torch.equal(o, o2) and torch.equal(S, S2) and all(torch.equal(g[n], g2[n]) for n in g)
     ops.device_status()
+
+
+@pytest.mark.parametrize("L,H,dk,dv", [(1, 1, 64, 128), (1, 2, 32, 64), (4, 1, 128, 64), (90, 2, 96, 40), (128, 1, 128, 128)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_a_lone_chunk_with_a_state_rounds_its_outputs_only(L, H, dk, dv, packed):
+    """The same for the state that such a sequence starts from, its outputs and its gradients; more items than SMs and
+    longer sequences between them."""
+    n = 90
+    x = make(L + dv, (n, L), H, H, dk, dv, torch.bfloat16, init=True, grads=True)
+    cu = list(range(0, n * L + 1, L)) if packed else None
+    if packed:
+        for name in ("q", "k", "v", "do"):
+            x[name] = x[name].flatten(0, 1)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, S = (ops.linear_attn_prefill_varlen(*args, cu, x["init"]) if packed else ops.linear_attn_prefill(*args, x["init"]))
+    g = ops.linear_attn_backward(*args, x["do"], x["init"], x["d_final"], cu_seqlens=cu)
+    ops.device_status()
+    wo, wS, mo, mS = lo.prefill(*args, dk ** -0.5, x["init"], cu)
+    want, mag = lo.backward(*args, dk ** -0.5, x["do"], x["init"], x["d_final"], cu)
+    check_state(S, wS, mS, L, dk, "final_state")
+    for got, w, m in [(o, wo, mo)] + [(g[name], want[name], mag[name]) for name in "qkv"]:
+        # two parts each of scores and of the state are off by 2^-16 of themselves
+        assert (np.abs(np64(got) - w) <= U * np.abs(w) * 1.001 + (2.0 ** -15 + n_terms(L, max(dk, dv)) * E) * m).all()
+
+
+def test_lone_chunks_between_longer_sequences():
+    """Sequences of one chunk, of more and of none in one CTA's hands, one behind the other."""
+    lens = [1, 300, 0, 5, 128, 129, 2, 700, 64] * 12
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x = make(21, (cu[-1],), 4, 2, 64, 64, torch.bfloat16, nseq=len(lens), init=True, grads=True)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, S = ops.linear_attn_prefill_varlen(*args, cu, x["init"])
+    g = ops.linear_attn_backward(*args, x["do"], x["init"], x["d_final"], cu_seqlens=cu)
+    ops.device_status()
+    wo, wS, mo, mS = lo.prefill(*args, 0.125, x["init"], cu)
+    check_out(o, wo, mo, torch.bfloat16, 700, 64, "o")
+    check_state(S, wS, mS, 700, 64, "final_state")
+    want, mag = lo.backward(*args, 0.125, x["do"], x["init"], x["d_final"], cu)
+    for name in "qkv":
+        check_out(g[name], want[name], mag[name], torch.bfloat16, 700, 64, "d" + name)
+    check_state(g["init_state"], want["init_state"], mag["init_state"], 700, 64, "d_init_state")
