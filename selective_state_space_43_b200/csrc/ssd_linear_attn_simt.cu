@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(threads<MODE>(), 2) scan_simt_kernel(ScanArgs 
                     sP[i * PP + j] = j <= i ? (p[ii][jj].x + p[ii][jj].y) * a.qk_scale * sPow[i - j] : 0.f;
                 }
             group_sync();
-            for (int j = 0; j < r0 + 4; j += 4) {
+            for (int j = 0; j < r0; j += 4) {
                 float4 pp[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) pp[i] = lds4(sP + (r0 + i) * PP + j);
@@ -159,6 +159,13 @@ __global__ void __launch_bounds__(threads<MODE>(), 2) scan_simt_kernel(ScanArgs 
                     axpy4(out[i], pp[i].z, x2);
                     axpy4(out[i], pp[i].w, x3);
                 }
+            }
+            // the diagonal's four: a later row's value is not multiplied by zero but left out, since it may not be finite
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = lds4(sV + (r0 + j) * PV + c4);
+#pragma unroll
+                for (int i = j; i < 4; ++i) axpy4(out[i], sP[(r0 + i) * PP + r0 + j], x);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
