@@ -398,9 +398,10 @@ SSD_API ssd_status ssd_set_timing_events(void* before_main, void* after_main);
  *     S_t = e^{log_decay[h]} S_{t-1} + k_t v_t^T
  *     o_t = scale * q_t S_t
  * The decay is a constant of the layer (log_decay <= 0, -inf keeps nothing of
- * the past); it has no gradient here.  A non-finite value in a row reaches the
- * other rows of its own sequence and head only: its later ones, and earlier
- * ones of up to 127 rows before.
+ * the past); it has no gradient here.  A NaN or an infinity reaches what depends
+ * on it and nothing else (a value in row t: outputs of t and later rows and the
+ * final state of its sequence and heads), whose values become NaN or infinite,
+ * which of the two is not said.  Scores that overflow count as infinite.
  *
  *   key_dim, value_dim  Dk, Dv: multiples of 8 from 8 to 128
  *   dtype               SSD_BF16 or SSD_F32 (q, k, v, o and their gradients);
@@ -449,8 +450,8 @@ SSD_API ssd_status ssd_linear_attn_prefill(const ssd_linear_attn_dims* dims, ssd
  * Gradients of the chunked form: of sum(d_o * o) + sum(d_final_state * final_state).
  * q, k, v, d_o contiguous; dq, dk, dv (out) laid out as q, k, v in dtype (shared key
  * and value heads: the sum over their query heads, taken in fp32).  init_state and d_final_state may be
- * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.  A non-finite value reaches the
- * gradients of its own sequence and head only.
+ * NULL (zeros); d_init_state (out) NULL when not wanted.  Deterministic.  A NaN or an infinity reaches the
+ * gradients that depend on it only, as in the forward.
  */
 SSD_API size_t ssd_linear_attn_backward_workspace_bytes(const ssd_linear_attn_dims* dims, ssd_dtype dtype, int packed);
 SSD_API ssd_status ssd_linear_attn_backward(const ssd_linear_attn_dims* dims, ssd_dtype dtype, const float* log_decay,

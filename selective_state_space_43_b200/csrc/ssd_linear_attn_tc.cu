@@ -21,6 +21,12 @@
 // into bf16 parts of 8 bits (v w = hi + mid + lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits)
 // where what the second leaves would show in a state that the caller gets, so that such a state is as exact as fp32 sums.
 //
+// Values that are not finite: what the mask multiplies by zero (scores behind the diagonal, and in P V the rows behind an
+// output's own) may be NaN or infinite, and would make outputs NaN that do not depend on it.  A product of such a value with
+// zero is NaN, so no output that is finite is wrong: the warps that write them watch for NaN, and an item that had one is done
+// again carefully.  There the scores behind the diagonal become zero before the mask, one warp takes what is not finite
+// out of V before P V, and Y1 starts as NaN where an output depends on it, else as zero.
+//
 // 28 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
 //   8-15  V' (shared memory -> shared memory), 32 channels each; the same threads zero the rows behind a sequence's end
@@ -30,7 +36,8 @@
 //         32 channels each
 //   24    TMA: K, V, Q of a chunk, two or three stages
 //   25    tcgen05.mma
-//   26    the CTA's items (27 only completes the warpgroup)
+//   26    the CTA's items
+//   27    V without what is not finite, of the items that are done again
 // Q, K, V are read once (Q and K once for each 64 value channels, the second time from L2), o written once.  Where heads
 // are many the power limit bounds it: 2 x 8192 rows of 74 heads 128 x 64 take 195 us (4.8 TB/s) at the 1365 MHz that it
 // leaves, and 152 us (6.1 TB/s) on zeros, which draw less, at 1965 MHz; 4 x 8192 rows of 64 heads 354 us.  Where they are
@@ -60,13 +67,20 @@ constexpr uint32_t OFF_BAR = OFF_S + kBox;
 constexpr uint32_t OFF_STOP = OFF_BAR + 256, OFF_TMEM = OFF_BAR + 264, OFF_ANSWER = OFF_BAR + 272, OFF_ITEM = OFF_BAR + 288;
 constexpr uint32_t OFF_ORDER = OFF_BAR + 512;
 constexpr int kSorted = 64;   // packed sequences that are taken longest first
-constexpr uint32_t kSmemBytes = OFF_ORDER + kSorted + 1024;  // + alignment of the base
+// The first row of a chunk, in scan order, with a value in a channel of V that is not finite (C: none); how many items are to be
+// done again, how many of them were while others were left, four items' notes of it (an item's is cleared by the one
+// before it), and the queue of them.
+constexpr uint32_t OFF_WILD = OFF_ORDER + kSorted, OFF_REDO = OFF_WILD + DVB * 4, OFF_QUEUE = OFF_REDO + 32;
+constexpr int kQueue = 8;     // no more than the ring's places are unfinished when the item warp looks, and as many when it has
+constexpr uint32_t kSmemBytes = OFF_QUEUE + kQueue * 52 + 1024;  // + alignment of the base
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
 // KFREE, QFREE, VFREE: the products that read a stage's tile are complete.
 // PREADY: without outputs, where there are no scores, V' is ready in its second place (VREADY: in its first).  One barrier for
 // both would be completed twice before the products' warp looks, and take a fast warp's arrival for a slow one's.
 constexpr int kStages = 3;  // at most
 enum Bar { FULL = 0, KFREE = 3, QFREE = 6, VFREE = 9, DSFULL = 12, DSREAD = 14, PFULL = 16, PREADY, VREADY, SREADY, Y2DONE, YFULL,
-           EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3 };
+           EPI, MMADONE, NEXT, LASTLOAD, IFULL, IEMPTY = IFULL + 3, kBars = IEMPTY + 3,
+           GUARD = DSREAD, AGREE };  // with outputs, where dS is not waited for
 static_assert(kBars * 8 <= 256, "the barriers' place");
 // TMEM columns: scores (their bf16 form takes the place of each 16), Y1, Y2, dS (two buffers of two parts)
 constexpr uint32_t COL_P = 0, COL_Y1 = 128, COL_Y2 = 192, COL_DS = 256;
@@ -90,22 +104,35 @@ template <int N> __device__ __forceinline__ void regs_more() {
 template <int N> __device__ __forceinline__ void regs_fewer() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// Waits for the phase of `parity`, for so many clock cycles at most; false when they have passed, or at once when *stop is set.
+// The roles wait at some forty places, each a copy of this: the kernel's speed depends on its code's size (with a wait of
+// twice the instructions 4 x 1000 rows of 32 heads 128 x 128 take 46 us instead of 44).
+constexpr int64_t kWait = 4000000000;        // 2 s at 1965 MHz
+constexpr int64_t kItemWait = 50 * kWait;    // the longest item is a whole sequence
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* stop, int64_t cycles = kWait) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const int64_t t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if ((stop && *stop) || clock64() - t0 > cycles) return false;
+    return true;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, stop));
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, stop));
 }
 // A CTA's work: one (64 value channels, head, sequence or segment) behind the other.  The item warp announces
 // them in a ring of kItems places that the other roles read in the same order, each at its own pace.
 constexpr int kItems = 3;
-constexpr uint64_t kItemWait = 100000000000ull;  // 100 s: the longest item is a whole sequence
 struct Item {
     int scan, h, dv0;  // scan < 0: no more
     int slot, seq;
     int row0, nc, last;  // first row, chunks, rows of the chunk that ends the sequence (or segment)
     int third;           // the last chunks, in scan order, whose V' needs its third part
     int rev;
+    int careful;         // done again, see above
+    int index;           // among the CTA's items
     float l;
 };
-static_assert(sizeof(Item) * kItems <= 512 - 288, "the ring's place");
+static_assert(sizeof(Item) * kItems <= 512 - 288 && sizeof(Item) <= 52, "the ring's place and the queue's");
 // The ring of tile stages, as each role follows it.  A stage is the K boxes (one per 64 of Dk), the V box and the Q
 // boxes of a chunk: three boxes or fewer leave room for three stages, Q and K of Dk > 64 for two.  Where the next
 // item's stages are cut differently the ring starts over at stage 0, when the loads have seen all others out.
@@ -130,18 +157,6 @@ struct Ring {
     __device__ __forceinline__ uint32_t v(bool q) const { return k(q) + kb * kBox; }
     __device__ __forceinline__ uint32_t q(bool has) const { return v(has) + kBox; }
 };
-// Whether the phase is complete, without waiting (try_wait suspends the thread for a while).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -240,6 +255,52 @@ __device__ __forceinline__ int64_t next_block(const void* answer) {
     return got ? (int64_t)x : -1;
 }
 
+// For items that are done again, by one warp: what is not finite in a V tile becomes zero, and `first` the first row, in scan
+// order, that had such a value in each channel.
+__device__ __forceinline__ void tame(uint8_t* tv, int* first, int lane, bool rev) {
+    first[lane] = first[lane + 32] = C;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < C * DVB / 2; i += 32) {  // words of two channels
+        const int row = i / 32, word = i & 31, at = rev ? C - 1 - row : row;
+        uint32_t* p = reinterpret_cast<uint32_t*>(tv + sw128_off(row, word / 4)) + (word & 3);
+        const uint32_t x = *p;
+        const bool lo = (x & 0x7F80u) == 0x7F80u, hi = (x & 0x7F800000u) == 0x7F800000u;
+        if (!lo && !hi) continue;
+        if (lo) atomicMin(first + 2 * word, at);
+        if (hi) atomicMin(first + 2 * word + 1, at);
+        *p = x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
+    }
+}
+// The same, by the warps of the scores: Y1 (32 of its channels) NaN where an output depends on such a value, else zero.
+__device__ __forceinline__ void start_y1(uint32_t y1, const int* first, int at) {
+#pragma unroll 1
+    for (int d = 0; d < 32; d += 8) {
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = first[d + i] <= at ? 0x7FC00000u : 0u;
+        tmem_st8(y1 + d, r);
+    }
+}
+// Of 64 columns of the scores, from tile column j0 on, those from n on become zero (rows behind the sequence's end, whatever they
+// hold), and with `careful` those behind the diagonal.
+__device__ __forceinline__ void trim(uint32_t p, int row, int j0, int n, bool careful, bool rev) {
+#pragma unroll 1
+    for (int j = careful ? 0 : max(0, (n - j0) & ~7); j < 64; j += 8) {
+        float v[8];
+        tmem_ld8(p + j, v);
+        tmem_wait_ld();
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = j0 + j + i;
+            r[i] = c < n && !(careful && (rev ? c < row : c > row)) ? __float_as_uint(v[i]) : 0u;
+        }
+        tmem_st8(p + j, r);
+    }
+    tmem_wait_st();
+}
+
 // kMode: see Mode.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_constant__ Params prm) {
@@ -249,6 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
     uint8_t* answer = sm + OFF_ANSWER;
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
+    Item* queue = reinterpret_cast<Item*>(sm + OFF_QUEUE);
+    volatile int* posted = reinterpret_cast<volatile int*>(sm + OFF_REDO);
+    volatile int *odd = posted + 4, *served = posted + 1;
+    uint64_t* asked = reinterpret_cast<uint64_t*>(sm + OFF_REDO + 8);  // a barrier: the warps of the scores want V
+    int* wild = reinterpret_cast<int*>(sm + OFF_WILD);
     constexpr bool kOut = kMode != kStates;
     constexpr int kMaxParts = kMode == kOutputs ? 2 : 3;  // of V'
     constexpr int kVWarps = kOut ? 8 : 16;
@@ -258,10 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         if (lane == 0) {
             for (int i = 0; i < kBars; ++i)
                 mbar_init(&bars[i], i == VREADY || (!kOut && i == PREADY) ? kVWarps
-                                    : i == PREADY || i == SREADY || i == EPI || i == DSREAD || i == DSREAD + 1 ? 8
-                                    : i >= IEMPTY ? 26  // warps that read an item
+                                    : i == PREADY || i == SREADY || i == EPI || i == AGREE || (!kOut && i == DSREAD) ? 8
+                                    : i >= IEMPTY ? (kOut ? 27 : 26)  // warps that read an item
                                                   : 1);
+            mbar_init(asked, 8);
             *stop = 0;
+            *posted = *served = 0;
+            for (int i = 0; i < 4; ++i) odd[i] = 0;
             fence_mbar_init();
         }
         __syncwarp();
@@ -275,18 +344,33 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
 
-    // A place of the ring, for a whole warp (lanes agree) or for one lane alone; nullptr: no more.  It is given back by
-    // leave(), after the role has copied what it needs.
-    auto enter = [&](int number, bool whole_warp) -> const Item* {
-        const int i = number % kItems;
-        bool ok = mbar_wait(&bars[IFULL + i], (number / kItems) & 1, stop, kItemWait);
-        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
-        if (!ok) *stop = 1;
-        return ok && items[i].scan >= 0 ? &items[i] : nullptr;
+    // The end of a round, for all warps; true: of the last.  The second round is for the items that are to be done again and were
+    // not yet when the first ended.
+    int round = 0;
+    auto over = [&] {
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        return !kOut || round++ == 1 || *posted == *served || *stop;
     };
-    auto leave = [&](int number, bool whole_warp) {
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) mbar_arrive(&bars[IEMPTY + number % kItems]);
+    // Gives back a place of the ring, after the role has copied what it needs.
+    auto leave = [&](int number) { warp_arrive(&bars[IEMPTY + number % kItems], lane); };
+    // A place of the ring, or nullptr: no more, and the last round is over.
+    auto enter = [&](int& number) -> const Item* {
+        for (;; ++number) {
+            const int i = number % kItems;
+            const bool ok = __all_sync(0xffffffffu, bar_wait(&bars[IFULL + i], (number / kItems) & 1, stop, kItemWait));
+            if (ok && items[i].scan >= 0) return &items[i];
+            if (!ok) *stop = 1;
+            if (over()) return nullptr;
+            leave(number);
+        }
+    };
+    // Of a role one of whose waits gave up.
+    auto give_up = [&] {
+        *stop = 1;
+        over();
     };
     // Whether the scores are kept in two bf16 parts: a lone chunk may have few outputs, which all share a score's error.
     auto two_parts = [](int nc) { return nc == 1; };
@@ -320,18 +404,33 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            if (lane == 0) {
+            int put = 0, taken = 0;  // announced (the first round's end too), and of the queue of items to be done again
+            do {
+                if (lane != 0) continue;
                 int64_t block = blockIdx.x;
-                int put = 0;
                 auto announce = [&](const Item& it) {
                     const int i = put % kItems;
-                    if (put >= kItems && !mbar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
+                    if (put >= kItems && !bar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
                     items[i] = it;
+                    items[i].index = put - round;
                     mbar_arrive(&bars[IFULL + i]);
                     ++put;
                     return true;
                 };
-                for (int asked = 0;; ++asked) {
+                // the loads of the item announced last are due to end
+                auto loaded = [&] { return bar_wait(&bars[LASTLOAD], (put - round - 1) & 1, stop, kItemWait); };
+                auto again = [&] {
+                    while (kOut && taken != *posted) {
+                        __threadfence_block();
+                        Item it = queue[taken++ % kQueue];
+                        it.careful = 1;
+                        if (!announce(it) || !loaded()) return false;
+                    }
+                    return true;
+                };
+                bool ok = true;
+                if (round == 1) ok = again();
+                for (int asks = 0; round == 0; ++asks) {
                     Item it;
                     it.scan = 0;
                     unsigned b = (unsigned)block;
@@ -351,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     it.last = (int)(g.n - (int64_t)(it.nc - 1) * C);
                     it.l = a.log_decay[it.h];
                     it.rev = a.reverse;
+                    it.careful = 0;
                     // What the second part leaves (2^-16) shows in a state that the caller gets unless at least d rows follow
                     // with e^{l d} < 2^-8: l d < -6.
                     it.third = kMode == kOutputs || (kMode == kWhole && !a.final_state) ? 0
@@ -358,21 +458,22 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                             : 1 << 30;
                     // the next block is taken only when this item's last three loads are due: early enough to be announced
                     // by then, late enough that none waits here while another SM is idle
-                    bool ok = !g.ok || (announce(it) && mbar_wait(&bars[LASTLOAD], (put - 1) & 1, stop, kItemWait));
+                    ok = (!g.ok || (announce(it) && loaded())) && again();
                     if (ok) {
                         mbar_arrive_expect_tx(&bars[NEXT], 16);
                         ask_next_block(answer, &bars[NEXT]);
-                        ok = mbar_wait(&bars[NEXT], asked & 1, nullptr);
+                        ok = bar_wait(&bars[NEXT], asks & 1, nullptr);
                         block = next_block(answer);
                         fence_async_smem();  // read before the next answer is written
                     }
-                    if (!ok) *stop = 1;
                     if (!ok || block < 0) break;
                 }
+                *served = taken;
+                if (!ok) *stop = 1;
                 Item end;
                 end.scan = -1;
                 if (!announce(end)) *stop = 1;
-            }
+            } while (!over());
         } else if (warp == kWarpTma) {
             // ---- tile loads.  The whole warp runs this loop, so that addresses stay in uniform registers; one elected lane
             // issues.
@@ -381,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             // a place's products are complete (at once where there were none)
             auto freed = [&](int bar, int i) { return warp_wait(&bars[bar + i], ((ring.phases >> i) & 1) ^ 1, stop); };
             bool ok = true;
-            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+            for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
                 const Scan& scan = prm.scan[__shfl_sync(0xffffffffu, it->scan, 0)];
                 const ScanArgs& a = scan.a;
                 const int dv0 = __shfl_sync(0xffffffffu, it->dv0, 0), nc = __shfl_sync(0xffffffffu, it->nc, 0);
@@ -389,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 auto stored = [&](int group) { return group == 1 ? h : h / group; };  // the stored head of a role
                 const int hk = stored(a.gk), hv = a.gv == a.gk ? hk : stored(a.gv), hq = kOut ? stored(a.gq) : 0;
                 const bool rev = a.reverse;
-                leave(k, true);
+                leave(k);
                 if (ring.cut(a.Dk, kOut) && k > 0)
                     for (int i = 0; i < kStages; ++i)
                         ok = ok && freed(KFREE, i) && (!kOut || freed(QFREE, i)) && freed(VFREE, i);
@@ -419,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     ring.step();
                 }
             }
-            if (!ok) *stop = 1;
+            if (!ok) give_up();
             // no load may be in flight when the CTA exits (each was consumed, unless a wait gave up)
-            for (int i = 0; i < kStages; ++i) mbar_wait(&bars[FULL + i], ((ring.phases >> i) & 1) ^ 1, nullptr, 100000000ull);
+            for (int i = 0; i < kStages; ++i) bar_wait(&bars[FULL + i], ((ring.phases >> i) & 1) ^ 1, nullptr, kWait / 20);
         } else if (warp == kWarpMma) {
             // ---- products.  The whole warp runs this loop, so that descriptors stay in uniform registers; one elected
             // lane issues.
@@ -434,12 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             Ring ring;
             const Item* it;
             bool ok = true;
-            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+            for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
                 ring.cut(prm.scan[it->scan].a.Dk, kOut);
                 const bool wide = ring.kb == 2;
                 const int nc = it->nc, third = it->third;
-                const bool twice = two_copies(prm.scan[it->scan].a, nc);
-                leave(k, true);
+                const bool twice = two_copies(prm.scan[it->scan].a, nc), careful = it->careful;
+                leave(k);
                 for (int c = 0; ok && c < nc; ++c, ++cc, ring.step()) {
                     const int s = ring.s;
                     // opaque to the compiler: descriptors are made where they are used, a few uniform adds each, instead
@@ -502,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)  // the bf16 scores: 16 to the first 8 of every 16 columns
-                                mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + k * 16, dV + k * 128, ID_Y, k > 0);
+                                mma_bf16_ts(tmem + COL_Y1, tmem + COL_P + k * 16, dV + k * 128, ID_Y, k > 0 || careful);
                             if (two_parts(nc)) {  // and what they leave, in the other 8
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)
@@ -529,26 +630,48 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     __syncwarp();
                 }
             }
-            if (!ok) *stop = 1;
+            if (!ok) give_up();
             // nothing may still be running on the tensor cores when TMEM is released
             if (elect_one()) mma_commit(&bars[MMADONE]);
             __syncwarp();
-            mbar_wait(&bars[MMADONE], 0, nullptr, 100000000ull);
+            bar_wait(&bars[MMADONE], 0, nullptr, kWait / 20);
+        } else if (kOut) {
+            // ---- V of items that are done again, when the warps of the scores ask for it: they follow every chunk, while this one
+            // skips other items' and is ahead of them, so that the parity of another barrier would tell it nothing
+            int gc = 0;  // chunks of such items
+            Ring ring;
+            const Item* it;
+            bool ok = true;
+            for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
+                ring.cut(prm.scan[it->scan].a.Dk, kOut);
+                const int nc = it->nc, rev = it->rev, careful = it->careful;
+                leave(k);
+                for (int c = 0; ok && c < nc; ++c, ring.step()) {
+                    if (!careful) continue;
+                    if (!(ok = warp_wait(asked, gc++ & 1, stop))) break;
+                    tame(sm + ring.v(kOut), wild, lane, rev);
+                    fence_async_smem();
+                    warp_arrive(&bars[GUARD], lane);
+                }
+            }
+            if (!ok) give_up();
+        } else {
+            over();
         }
     } else if (kOut && warp < 8) {
         if constexpr (kOut) {
             regs_more<112>();
             // ---- scores: row `row`, columns 64 half .. 64 half + 63 ----
             const int j0 = (warp >> 2) * 64;
-            int cc = 0;
+            int cc = 0, gc = 0;  // chunks, those of items that are done again
             const Item* it;
             bool ok = true;
-            for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+            for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
                 const ScanArgs& a = prm.scan[it->scan].a;
                 const int nc = it->nc, last = it->last;
                 const float l = it->l;
-                const bool rev = a.reverse;
-                leave(k, true);
+                const bool rev = a.reverse, careful = it->careful;
+                leave(k);
                 // one factor e^l per step away from the diagonal (off by 127 fp32 roundings at most, far below bf16's)
                 float m[64];
                 const float el = decay_pow(l, 1);
@@ -572,6 +695,16 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     if (!(ok = warp_wait(&bars[PFULL], cc & 1, stop))) break;
                     tc_fence_after();
                     const uint32_t col = lane_base + COL_P + j0;
+                    if (careful) {  // V' is made of V (dS is complete), and the outputs before have been read from Y1
+                        ok = warp_wait(&bars[DSFULL + (cc & 1)], (cc >> 1) & 1, stop) &&
+                             (cc == 0 || warp_wait(&bars[EPI], (cc - 1) & 1, stop));
+                        if (!ok) break;
+                        warp_arrive(asked, lane);
+                        if (!(ok = warp_wait(&bars[GUARD], gc++ & 1, stop))) break;
+                        tc_fence_after();
+                        start_y1(lane_base + COL_Y1 + j0 / 2, wild + j0 / 2, rev ? C - 1 - row : row);
+                    }
+                    if (careful || n < j0 + 64) trim(col, row, j0, n, careful, rev);
 #pragma unroll
                     for (int b = 0; b < 4; b += 2) {
                         float v[2][16];
@@ -582,10 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         for (int i = 0; i < 2; ++i) {
                             uint32_t p[8];
                             const int j1 = (b + i) * 16;
-                            if (n < C) {  // columns behind the sequence's end are not its own, whatever they hold
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) v[i][j] = j0 + j1 + j < n ? v[i][j] : 0.f;
-                            }
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const float2 f = __fmul2_rn(make_float2(v[i][2 * j], v[i][2 * j + 1]),
@@ -608,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     warp_arrive(&bars[PREADY], lane);
                 }
             }
-            if (!ok) *stop = 1;
+            if (!ok) give_up();
         }
     } else if (warp < kWarpOut) {
         // ---- V': tile row `row`, 64 * 4 / kVWarps of the 64 channels ----
@@ -619,13 +748,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
         Ring ring;
         const Item* it;
         bool ok = true;
-        for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+        for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
             const ScanArgs& a = prm.scan[it->scan].a;
             ring.cut(a.Dk, kOut);
             const int nc = it->nc, last = it->last, third = it->third;
             const float l = it->l, w_scale = a.w_scale;
             const bool rev = a.reverse;
-            leave(k, true);
+            leave(k);
             // weight of tile row `row` in the state behind a chunk of n rows
             auto weight = [&](int n) { return row < n ? w_scale * decay_pow(l, rev ? row + 1 : n - 1 - row) : 0.f; };
             const float w_full = weight(C);
@@ -688,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 warp_arrive(&bars[kOut || !(cc & 1) ? VREADY : PREADY], lane);
             }
         }
-        if (!ok) *stop = 1;
+        if (!ok) give_up();
     } else {
         // ---- S: key row `row`, and the outputs: tile row `row`; 32 of the 64 channels ----
         regs_more<kOut ? 80 : 88>();
@@ -718,7 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             ++sc;
         };
         // the item is read from its place in the ring wherever it is needed, not kept in registers
-        for (int k = 0; ok && (it = enter(k, true)) != nullptr; ++k) {
+        for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
+            bool finite = true;  // this thread's outputs
             const float decay_full = decay_pow(it->l, C);
             // this row of the state, where it is kept: among the sequences' or the segments'
             auto state_row = [&](const float* base, bool transposed) {
@@ -791,10 +921,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     // a thread stores its own row: 32-byte stores fill whole sectors where the rows allow them
                     const int esize = a.o_f32 ? 4 : 2, stored = row < n ? live : 0;
                     const bool wide = a.Dv * esize % 32 == 0 && (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+                    float2 zero = make_float2(0.f, 0.f);  // sums of 0 x output: NaN where one is not finite
                     uint8_t* dst = static_cast<uint8_t*>(a.o) +
                                    (((int64_t)it->row0 + place * C + row) * a.H * a.Dv + (int64_t)it->h * a.Dv + it->dv0 +
                                     half * kHalf) * esize;
-#pragma unroll
+#pragma unroll 1
                     for (int b = 0; b < kHalf / 16; ++b) {
                         float x[16], y[16];
                         tmem_ld16(lane_base + COL_Y1 + half * kHalf + b * 16, x);
@@ -810,12 +941,31 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                 __ffma2_rn(make_float2(e, e), make_float2(y[j], y[j + 1]), make_float2(x[j], x[j + 1]));
                             x[j] = f.x;
                             x[j + 1] = f.y;
+                            zero = __ffma2_rn(f, make_float2(0.f, 0.f), zero);
                         }
                         if (a.o_f32)
                             store16(reinterpret_cast<float*>(dst) + b * 16, x, stored - b * 16, wide);
                         else
                             store16(reinterpret_cast<__nv_bfloat16*>(dst) + b * 16, x, stored - b * 16, wide);
                     }
+                    finite = finite && (stored <= 0 || zero.x + zero.y == 0.f);
+                }
+            }
+            if (kOut && ok) {
+                // Done again by all warps or by none: the final state, which may take the initial one's place, is left until then.
+                const int item = it->index;
+                if (!__all_sync(0xffffffffu, finite) && lane == 0) odd[item & 3] = 1;
+                if (warp == kWarpOut && lane == 0) odd[(item + 1) & 3] = 0;
+                warp_arrive(&bars[AGREE], lane);
+                ok = warp_wait(&bars[AGREE], item & 1, stop);
+                if (ok && odd[item & 3] && !it->careful) {
+                    if (warp == kWarpOut && lane == 0) {
+                        queue[*posted % kQueue] = *it;
+                        __threadfence_block();
+                        *posted = *posted + 1;
+                    }
+                    leave(k);
+                    continue;
                 }
             }
             if (kMode != kOutputs) {
@@ -828,13 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (d < live) *reinterpret_cast<float4*>(dst + d) = make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]);
                 }
             }
-            leave(k, true);
+            leave(k);
         }
-        if (!ok) *stop = 1;
+        if (!ok) give_up();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
     if (tid == 0 && *stop) atomicOr(prm.scan[0].a.err, kErrTimeout);
 }

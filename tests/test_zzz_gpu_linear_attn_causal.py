@@ -10,9 +10,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from selective_state_space_43_b200 import ops  # noqa: E402
-from test_zzz_gpu_linear_attn import make, workspace_bytes  # noqa: E402
-
-DTYPES = [torch.float32]
+from test_zzz_gpu_linear_attn import DTYPES, make, workspace_bytes  # noqa: E402
 
 NAN, INF = float("nan"), float("inf")
 
@@ -20,7 +18,9 @@ NAN, INF = float("nan"), float("inf")
 def clean_and_dirty(x, name, where, value, call):
     y = {k: None if v is None else v.clone() for k, v in x.items()}
     y[name][where] = value
-    return call(x), call(y)
+    out = call(x), call(y)
+    ops.device_status()
+    return out
 
 
 def check(got, clean, touched, what):
@@ -140,3 +140,55 @@ def test_rows_behind_a_padded_prompt(dtype):
                 y[name][:, end:] = value
             o2, _ = ops.linear_attn_prefill(y["q"], y["k"], y["v"], y["log_decay"])
             assert torch.equal(o[:, :end], o2[:, :end]), (end, value)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("share", [0.02, 0.5, 1.0])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 96)])
+def test_many_sequences_some_of_them_padded(dk, dv, share, dtype):
+    """More sequences than SMs, in place: from a row on, some hold NaN in q, k, v (a batch padded with whatever was there)."""
+    g = torch.Generator().manual_seed(5)
+    H, Hk, n = 4, 2, 260
+    lens = [(0, 1, 5, 100, 128, 129, 300)[int(i)] for i in torch.randint(0, 7, (n,), generator=g)]
+    cu = [0]
+    for m in lens:
+        cu.append(cu[-1] + m)
+    offsets = torch.tensor(cu).cuda()
+    x = make(17, (cu[-1],), H, Hk, dk, dv, dtype, nseq=n, init=True, grads=True)
+    y = {k: v.clone() for k, v in x.items()}
+    padded = torch.zeros(n, dtype=torch.bool, device="cuda")
+    front = torch.ones(cu[-1], dtype=torch.bool, device="cuda")
+    for i, m in enumerate(lens):
+        if m and float(torch.rand((), generator=g)) < share:
+            row = int(torch.randint(0, m, (), generator=g))
+            padded[i] = True
+            front[cu[i] + row:cu[i + 1]] = False
+            for name in ("q", "k", "v"):
+                y[name][cu[i] + row:cu[i + 1]] = NAN
+    S = [z["init"].clone() for z in (x, y)]
+    o = [ops.linear_attn_prefill_varlen(z["q"], z["k"], z["v"], z["log_decay"], offsets, s, final_state=s)[0]
+         for z, s in zip((x, y), S)]
+    a, b = backward(x, offsets), backward(y, offsets)
+    ops.device_status()
+    assert torch.equal(o[0][front], o[1][front]) and not torch.isfinite(o[1][~front]).any()
+    assert torch.equal(S[0][~padded], S[1][~padded]) and not torch.isfinite(S[1][padded]).any()
+    assert torch.equal(a["q"][front], b["q"][front])
+    whole = torch.ones(cu[-1], dtype=torch.bool, device="cuda")  # rows of the sequences that hold no NaN
+    for i, m in enumerate(lens):
+        whole[cu[i]:cu[i + 1]] = not bool(padded[i])
+    for name in "kv":
+        assert torch.equal(a[name][whole], b[name][whole]), name
+    assert torch.equal(a["init_state"][~padded], b["init_state"][~padded])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scores_that_overflow_do_not_reach_earlier_rows(dtype):
+    """Keys so large that their scores are infinite although they are not, with values of zero."""
+    x = make(6, (2, 200), 2, 2, 64, 64, dtype)
+    o, _ = ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"])
+    y = {k: None if v is None else v.clone() for k, v in x.items()}
+    y["k"][:, 70:] = 3e38
+    y["v"][:, 70:] = 0
+    o2, _ = ops.linear_attn_prefill(y["q"], y["k"], y["v"], y["log_decay"])
+    ops.device_status()
+    assert torch.equal(o[:, :70], o2[:, :70])
