@@ -17,7 +17,7 @@
 // chunk before.
 //
 // Roundings: scores (times their decay) to bf16, the A operand of Y1; the copy of S that Y2 reads to bf16 (S itself stays
-// fp32); both to two bf16 parts in a sequence of one chunk, whose few outputs may share their errors; o once.  V' is cut
+// fp32); both to two bf16 parts in a sequence or segment of one chunk, whose few outputs may share their errors; o once.  V' is cut
 // into bf16 parts of 8 bits (v w = hi + mid + lo): two (16 bits) where S only feeds bf16 outputs, all three (24 bits)
 // where what the second leaves would show in a state that the caller gets, so that such a state is as exact as fp32 sums.
 //
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     auto two_parts = [](int nc) { return nc == 1; };
     // Whether the same holds for the state that its outputs start from: the copy of S is then written twice, what the first
     // leaves after the product with the first.
-    auto two_copies = [&](const ScanArgs& a, int nc) { return kMode == kWhole && two_parts(nc) && a.init; };
+    auto two_copies = [&](const ScanArgs& a, int nc) { return kOut && two_parts(nc) && (kMode == kOutputs || a.init); };
     // the place of chunk c, in scan order, among the item's chunks; the rows of the chunk at a place
     auto place_of = [](bool rev, int nc, int c) { return rev ? nc - 1 - c : c; };
     auto rows_of = [](int place, int nc, int last) { return place == nc - 1 ? last : C; };

@@ -1,0 +1,80 @@
+"""Linear attention on the GPU: how near its results are, where the token-by-token comparison alone would let more through.
+
+u = 2^-8 is half a bf16 step, relative; e = 2^-24 half an fp32 one.  Rounding a normal variable to bf16 is off by a value
+even in +-u 2^k where 2^k <= |x| < 2^(k+1): u / sqrt(3) sqrt(sum_k 4^k P_k) = 0.425 u of its norm.  A bf16 output is rounded
+once (0.425 u), and where its terms (a score, or an element of the state) are rounded once before, terms of random
+signs, by sqrt(2) 0.425 u = 0.60 u of the result's norm.
+"""
+import numpy as np
+import pytest
+import torch
+
+import linear_attn_oracle as lo
+
+pytestmark = pytest.mark.gpu
+
+from selective_state_space_43_b200 import ops  # noqa: E402
+from test_zzz_gpu_linear_attn import E, U, make, n_terms, np64, workspace_bytes  # noqa: E402
+
+
+def starts(lens, first=0):
+    cu = [first]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def check_state(got, want, mag, length, dk, what):
+    """Sums of fp32 roundings, every value finite."""
+    err, tol = np.abs(np64(got) - want), n_terms(length, dk) * E * mag + 1e-30
+    assert (err <= tol).all(), f"{what}: {(~(err <= tol)).sum()} of {err.size} off"
+
+
+def check_lone_chunk(got, want, mag, length, dk, what):
+    """Scores and the state that the outputs start from in two bf16 parts each, 2^-16 of themselves off: the outputs' own
+    rounding is all that shows."""
+    err = np.abs(np64(got) - want)
+    tol = U * np.abs(want) * 1.001 + (2.0 ** -15 + n_terms(length, dk) * E) * mag
+    assert (err <= tol).all(), f"{what}: {(~(err <= tol)).sum()} of {err.size} off, worst {np.max(err / (tol + 1e-30)):.2f}"
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 64), (96, 128), (40, 40)])
+def test_lone_chunks_of_a_cut_batch_round_their_outputs_only(dk, dv):
+    """Short sequences of a packed batch that is cut into segments: as exact as in a batch that is not."""
+    lens = [1, 4000, 2, 0, 4, 128, 1, 90, 3]
+    cu, H = starts(lens), 2
+    assert workspace_bytes(cu[-1], H, H, dk, dv, torch.bfloat16, True, len(lens)) > 0
+    assert workspace_bytes(cu[-1], H, H, dk, dv, torch.bfloat16, True, len(lens), True) > 0
+    x = make(dk + dv, (cu[-1],), H, H, dk, dv, torch.bfloat16, nseq=len(lens), init=True, grads=True)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, S = ops.linear_attn_prefill_varlen(*args, cu, x["init"])
+    g = ops.linear_attn_backward(*args, x["do"], x["init"], x["d_final"], cu_seqlens=cu)
+    ops.device_status()
+    wo, wS, mo, mS = lo.prefill(*args, dk ** -0.5, x["init"], cu)
+    want, mag = lo.backward(*args, dk ** -0.5, x["do"], x["init"], x["d_final"], cu)
+    check_state(S, wS, mS, 4000, dk, "final_state")
+    check_state(g["init_state"], want["init_state"], mag["init_state"], 4000, max(dk, dv), "d_init_state")
+    for i, n in enumerate(lens):
+        if n > 128:
+            continue
+        at = slice(cu[i], cu[i + 1])
+        check_lone_chunk(o[at], wo[at], mo[at], n, dk, f"o of sequence {i}")
+        for name in "qkv":
+            check_lone_chunk(g[name][at], want[name][at], mag[name][at], n, max(dk, dv), f"d{name} of sequence {i}")
+
+
+@pytest.mark.parametrize("L", [2049, 2100])
+def test_a_segment_of_one_chunk_rounds_its_outputs_only(L):
+    """A long sequence whose last segment (of 256, 512, 1024 or 2048 rows) is one chunk, from row 2048 on: it starts from a
+    joined state."""
+    H, dk, dv = 8, 64, 64
+    assert workspace_bytes(L, H, H, dk, dv, torch.bfloat16) > 0
+    x = make(L, (1, L), H, H, dk, dv, torch.bfloat16, init=True)
+    x["log_decay"][:] = -1e-3
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, S = ops.linear_attn_prefill(*args, x["init"])
+    wo, wS, mo, mS = lo.prefill(*args, dk ** -0.5, x["init"])
+    check_state(S, wS, mS, L, dk, "final_state")
+    err = np64(o)[:, 2048:] - wo[:, 2048:]
+    # one rounding is 0.425 u, two are 0.60 u; 512 values or more leave the former within a tenth (three deviations)
+    assert np.linalg.norm(err) <= 0.5 * U * np.linalg.norm(wo[:, 2048:])
