@@ -14,7 +14,7 @@ import linear_attn_oracle as lo
 pytestmark = pytest.mark.gpu
 
 from selective_state_space_43_b200 import ops  # noqa: E402
-from test_zzz_gpu_linear_attn import E, U, make, n_terms, np64, workspace_bytes  # noqa: E402
+from test_zzz_gpu_linear_attn import DTYPES, E, U, make, n_terms, np64, workspace_bytes  # noqa: E402
 
 
 def starts(lens, first=0):
@@ -78,3 +78,57 @@ def test_a_segment_of_one_chunk_rounds_its_outputs_only(L):
     err = np64(o)[:, 2048:] - wo[:, 2048:]
     # one rounding is 0.425 u, two are 0.60 u; 512 values or more leave the former within a tenth (three deviations)
     assert np.linalg.norm(err) <= 0.5 * U * np.linalg.norm(wo[:, 2048:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cu", [[0, 0, 1, 1, 130, 386, 386], [3, 3, 131, 260, 300], [5, 261, 2821, 2821, 3077, 4001]])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 40)])
+def test_states_among_rows_of_nan_are_finite(cu, dk, dv, dtype):
+    """States and gradients of states in packed batches whose buffers hold NaN outside every sequence; a workspace and
+    outputs that held NaN before."""
+    T, n, H, Hk = cu[-1] + 37, len(cu) - 1, 2, 1
+    x = make(sum(cu) + dk, (T,), H, Hk, dk, dv, dtype, nseq=n, init=True, grads=True)
+    clean = {k: v.clone() for k, v in x.items()}
+    for name in ("q", "k", "v", "do"):
+        x[name][cu[-1]:] = float("nan")
+        x[name][:cu[0]] = float("inf")
+    nan = float("nan")
+    need = max(workspace_bytes(T, H, Hk, dk, dv, dtype, True, n, b) for b in (False, True))
+    ws = torch.full((need // 4 + 4,), nan, device="cuda")
+    o = torch.full((T, H, dv), nan, device="cuda").to(dtype)
+    S = torch.full((n, H, dk, dv), nan, device="cuda")
+    ops.linear_attn_prefill_varlen(x["q"], x["k"], x["v"], x["log_decay"], cu, x["init"], workspace=ws, o=o, final_state=S)
+    ws.fill_(nan)
+    g = ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["d_final"], cu_seqlens=cu,
+                                 workspace=ws)
+    ops.device_status()
+    longest = max(b - a for a, b in zip(cu, cu[1:]))
+    args = [clean[k] for k in ("q", "k", "v", "log_decay")] + [dk ** -0.5]
+    _, wS, _, mS = lo.prefill(*args, x["init"], cu)
+    want, mag = lo.backward(*args, clean["do"], x["init"], x["d_final"], cu)
+    check_state(S, wS, mS, longest, dk, "final_state")
+    check_state(g["init_state"], want["init_state"], mag["init_state"], longest, max(dk, dv), "d_init_state")
+    assert torch.isfinite(o[cu[0]:cu[-1]]).all() and all(torch.isfinite(g[name][cu[0]:cu[-1]]).all() for name in "qkv")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_states_of_the_step_are_finite(dtype):
+    x = make(31, (33,), 4, 2, 40, 96, dtype, init=True)
+    state = x["init"].clone()
+    ops.linear_attn_decode_step(x["q"], x["k"], x["v"], x["log_decay"], state)
+    _, wS, _, mS = lo.prefill(x["q"][:, None], x["k"][:, None], x["v"][:, None], x["log_decay"], 40 ** -0.5, x["init"])
+    check_state(state, wS, mS, 1, 40, "state")
+
+
+@pytest.mark.parametrize("L,Hk,group,dk,dv", [(300, 3, 1, 128, 128), (1025, 2, 2, 64, 64), (2500, 2, 1, 64, 128)])
+def test_bf16_results_are_off_by_two_roundings(L, Hk, group, dk, dv):
+    x = make(L + 1, (1, L), Hk * group, Hk, dk, dv, torch.bfloat16, init=True, grads=True)
+    args = (x["q"], x["k"], x["v"], x["log_decay"])
+    o, _ = ops.linear_attn_prefill(*args, x["init"])
+    g = ops.linear_attn_backward(*args, x["do"], x["init"], x["d_final"])
+    wo, _, _, _ = lo.prefill(*args, dk ** -0.5, x["init"])
+    want, _ = lo.backward(*args, dk ** -0.5, x["do"], x["init"], x["d_final"])
+    for name, a, w in [("o", o, wo)] + [(n, g[n], want[n]) for n in "qkv"]:
+        rel = np.linalg.norm(np64(a) - w) / np.linalg.norm(w)
+        # 0.60 u, and a quarter over for terms that are not normal
+        assert rel <= 0.75 * U, (name, rel)
