@@ -132,3 +132,56 @@ def test_bf16_results_are_off_by_two_roundings(L, Hk, group, dk, dv):
         rel = np.linalg.norm(np64(a) - w) / np.linalg.norm(w)
         # 0.60 u, and a quarter over for terms that are not normal
         assert rel <= 0.75 * U, (name, rel)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_captured_steps_give_what_eager_ones_give(dtype):
+    """Prefill, two tokens and gradients in a graph, each run with states of its own; every output is compared."""
+    H, dk, dv = 4, 128, 64
+    x = make(2, (1, 700), H, 2, dk, dv, dtype, init=True, grads=True)
+    toks = [make(3 + i, (1,), H, 2, dk, dv, dtype) for i in range(2)]
+    names = ("q", "k", "v", "do", "init", "d_final")
+
+    def step(state):
+        o, S = ops.linear_attn_prefill(x["q"], x["k"], x["v"], x["log_decay"], x["init"])
+        state.copy_(S)
+        outs = [ops.linear_attn_decode_step(t["q"], t["k"], t["v"], x["log_decay"], state) for t in toks]
+        g = ops.linear_attn_backward(x["q"], x["k"], x["v"], x["log_decay"], x["do"], x["init"], x["d_final"])
+        return [o, S, state] + outs + [g["q"], g["k"], g["v"], g["init_state"]]
+
+    states = [torch.empty_like(x["init"]) for _ in range(3)]
+    step(states[2])
+    torch.cuda.synchronize()
+    graphs = []
+    for s in states[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(s)
+        graphs.append((g, out))
+    fresh = make(77, (1, 700), H, 2, dk, dv, dtype, init=True, grads=True)
+    for name in names:
+        x[name].copy_(fresh[name])
+    for t, seed in zip(toks, (78, 79)):
+        for name, v in make(seed, (1,), H, 2, dk, dv, dtype).items():
+            if name in ("q", "k", "v"):
+                t[name].copy_(v)
+    for s in states:
+        s.fill_(float("nan"))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for g, _ in graphs:
+            g.replay()
+    eager = step(states[2])
+    torch.cuda.synchronize()
+    ops.device_status()
+    for _, out in graphs:
+        for i, (a, b) in enumerate(zip(out, eager)):
+            assert torch.isfinite(b).all() and torch.equal(a, b), i
+    S = np64(eager[1])
+    for i, t in enumerate(toks):
+        w, S, m, mS = lo.prefill(t["q"][:, None], t["k"][:, None], t["v"][:, None], x["log_decay"], dk ** -0.5,
+                                 torch.from_numpy(S))
+        tol = n_terms(2, dk) * E * m[:, 0] + (U * np.abs(w[:, 0]) if dtype == torch.bfloat16 else 0)
+        assert (np.abs(np64(eager[3 + i]) - w[:, 0]) <= tol).all()
+    check_state(eager[2], S, mS + np.abs(S), 2, dk, "state")
