@@ -409,7 +409,10 @@ SSD_API ssd_status ssd_set_timing_events(void* before_main, void* after_main);
  *   rows                batch * seqlen, or seqlen alone when packed; < 2^31 - 256
  * Packed batches: cu_seqlens is a device array of batch + 1 non-decreasing row
  * offsets, sequence s = rows cu_seqlens[s] .. cu_seqlens[s+1]-1; rows outside
- * every sequence are neither used nor written.  Offsets out of order or out of
+ * every sequence are neither used nor written.  The work is divided by the number
+ * of sequences and rows alone (lengths are on the device), for prompts that differ
+ * as prompts do: one of thousands of rows among single tokens, on few heads, is
+ * faster in a call of its own.  Offsets out of order or out of
  * range are reported by ssd_device_status (SSD_ERR_SHAPE); no memory outside the
  * buffers is touched, and the outputs of that call are unspecified.
  */

@@ -244,52 +244,63 @@ cudaError_t launch_scans(const ScanArgs* scans, int count, Mode mode, cudaStream
 // A scan walks its rows one chunk behind the other, so a call with few (sequence, head) pairs leaves SMs
 // idle.  Cut into segments it takes two passes (the state each segment leaves, joined, then the outputs from
 // the joined states), which read keys and values twice.  The choice compares modelled times in microseconds: a block
-// costs `start`, and per row `row` for outputs and state or `state_row` for states alone; blocks run `slots` at a
-// time in each of a pass's launches; the cut adds two launches (`extra`) and the writing, joining and reading of its
-// states at `state_rate` bytes a microsecond.  Both sides of the rule as measured (B200, whole sequences against the
-// chosen cut): bf16, 1 x 8191 rows, 16 heads of 128 x 128: 138 against 72 us (2048 rows; 90 at 512); 4 x 8192 rows, 64
-// heads of 128 x 64: 294 us whole (450 at 2048 rows).  fp32, 1 x 256 rows, 4 heads of 32 x 64: 31 against 14 us (32
-// rows); 2 x 2048 rows, 8 heads of 128 x 128: 544 against 175 us (256 rows); 16 x 300 rows, 8 heads of 96 x 64: 74 us
-// whole (120 at 128 rows); 4 x 1000 rows, 32 heads of 128 x 128: 438 us whole (712 at 256 rows).
+// costs `start`, and per row `row` for outputs and state or `state_row` for states alone; an SM runs `resident` blocks
+// (`state_resident` of states alone) side by side, each of which slows the others by `beside`; the cut adds two launches
+// (`extra`) and the writing, joining and reading of its states at `state_rate` bytes a microsecond.  The first cut has to
+// gain what `cut` says, a shorter one what `shorter` says over a longer.
+//
+// The lengths of a packed batch are not known here (they are on the device): its longest sequence is taken to be `spread`
+// times the mean, each sequence to need `more` segments beside those of its rows.  The constants are fitted to 229 measured
+// cases (B200, every cut of 32 to 8192 rows; sizes drawn at random, packed rows cut at random places): in 224 of
+// them the choice is within 10 % of the fastest, the worst is 22 % off (bf16 backward, 2 sequences of 4932 rows, 8 heads of
+// 64 x 96: 54 us, 44 whole).  Both sides of some, in us as replayed one behind the other, whole against the chosen cut:
+// bf16, 1 x 8191 rows, 16 heads of 128 x 128, 120 against 72 (2048 rows; 90 at 512); 9000 rows in 12, 10 heads of
+// 64 x 64, 37 whole (51 at 512); 4 x 8192 rows, 64 heads of 128 x 64, 289 whole (459 at 2048).  fp32, 1 x 256 rows, 4 heads
+// of 32 x 64, 33 against 17 (32 rows); 4636 rows in 15, 16 heads of 64 x 96, 308 against 253 (128; 321 at 512);
+// backward of 4 x 1000 rows, 16 heads of 128 x 64, 736 against 598 (128; 575 at 256, 704 at 512); 4 x 1000 rows, 32 heads of
+// 128 x 128, 446 whole (705 at 256).
+//
+// A packed batch of one long sequence among many short ones looks like an even one from here, and stays whole where that
+// would be right: 32768 rows and 63 single ones, 8 heads of 128 x 64, 426 us whole (156 at 2048), but 32831 rows in 64 even
+// ones 66 whole (158 at 1024); 16384 rows and 31 single ones, 4 heads of 64 x 64, 203 (48 at 1024), even ones 33 (47).
 struct Cost {
-    double start, row, state_row, extra, state_rate, slots;
+    double start, row, state_row, extra, state_rate, beside, resident, state_resident, spread, more, cut, shorter;
     int64_t least;  // rows of a segment: a chunk of the kernel
     bool together;  // a pass's scans are one launch
 };
 Cost cost_of(bool bf16, int Dk) {
-    if (bf16) return Cost{5.0, 2.0 / 128, 1.2 / 128, 6.0, 5e6, 148.0, 256, true};
-    const double row = 0.06 + 0.0021 * Dk;
-    return Cost{5.0, row, 0.45 * row, 10.0, 2.5e6, Dk > 64 ? 220.0 : 450.0, 32, false};
+    if (bf16) return Cost{3.3, 1.46 / 128, 0.8 / 128, 6.0, 7.6e6, 0.0, 1.0, 1.0, 3.4, 0.68, 0.87, 0.84, 256, true};
+    const double row = 0.031 + 0.004 * Dk;
+    return Cost{0.9, row, 0.73 * row, 5.0, 2.6e6, 0.136, 2.0, 16.0, 4.4, 0.65, 0.8, 0.957, 32, false};
 }
+constexpr double kSms = 148.0;
 // Rows of a segment, or 0: whole sequences.  `blocks`: blocks of the output pass for each sequence, of `scans` scans;
 // `state_blocks`, `state_scans`: of the states' pass.
 int64_t segment_rows(int64_t batch, int64_t L, int64_t rows, bool packed, bool bf16, int Dk, int Dv, int64_t H,
                      int64_t blocks, int scans, int64_t state_blocks, int state_scans) {
     if (batch == 0 || rows == 0) return 0;
     const Cost k = cost_of(bf16, Dk);
-    const double mean = (double)rows / batch;
-    // the longest of a packed batch is not known here; four times the mean is usual for prompts
-    const double longest = packed ? fmin((double)rows, 4.0 * mean) : (double)L;
-    auto waves = [&](double n, int launches) {
-        if (k.together) launches = 1;
-        const double w = n / launches / k.slots;
-        return launches * (w <= 1.0 ? 1.0 : bf16 && !packed ? ceil(w) : w);
+    const double mean = (double)rows / batch, longest = packed ? fmin((double)rows, k.spread * mean) : (double)L;
+    // n blocks of `of` scans, rows_each rows in the mean and rows_most in the longest
+    auto pass = [&](double n, int of, double per_row, double rows_each, double rows_most, double resident) {
+        const int launches = k.together ? 1 : of;
+        const double on_sm = fmax(1.0, n / launches / kSms);
+        const double slower = 1.0 + k.beside * (fmin(on_sm, resident) - 1.0);
+        const double turns = fmax(1.0, on_sm / resident);
+        return launches * fmax((packed ? turns : ceil(turns)) * slower * (k.start + rows_each * per_row),
+                               k.start + rows_most * per_row);
     };
-    const int launches = k.together ? 1 : scans;
-    double best = fmax(waves((double)batch * blocks, scans) * (k.start + mean * k.row), launches * (k.start + longest * k.row));
+    double best = pass((double)batch * blocks, scans, k.row, mean, longest, k.resident);
     int64_t seg = 0;
     int64_t m = k.least;
     while (m * 2 < longest) m *= 2;
-    for (; m >= k.least && m < longest; m /= 2) {  // the longest that is not 10 % worse than a shorter one
-        const double slots = packed ? rows / (double)m + 0.5 * batch : batch * ceil((double)L / m);
+    for (; m >= k.least && m < longest; m /= 2) {
+        const double slots = packed ? rows / (double)m + k.more * batch : batch * ceil((double)L / m);
         const double bytes = slots * H * Dk * Dv * 4 * 4 * state_scans;  // written, read and written, read
         const double part = fmin((double)m, mean), most = fmin((double)m, longest);
-        auto pass = [&](double n, int of, double per_row) {
-            return fmax(waves(n, of) * (k.start + part * per_row), (k.together ? 1 : of) * (k.start + most * per_row));
-        };
-        const double t = pass(slots * state_blocks, state_scans, k.state_row) + pass(slots * blocks, scans, k.row) + k.extra +
-                         bytes / k.state_rate;
-        if (t < 0.9 * best) {
+        const double t = pass(slots * state_blocks, state_scans, k.state_row, part, most, k.state_resident) +
+                         pass(slots * blocks, scans, k.row, part, most, k.resident) + k.extra + bytes / k.state_rate;
+        if (t < (seg ? k.shorter : k.cut) * best) {
             best = t;
             seg = m;
         }
