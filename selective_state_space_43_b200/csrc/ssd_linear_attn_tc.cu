@@ -70,7 +70,7 @@ constexpr int kSorted = 64;   // packed sequences that are taken longest first
 // The first row of a chunk, in scan order, with a value in a channel of V that is not finite (C: none); how many items are to be
 // done again, how many of them were while others were left, four items' notes of it (an item's is cleared by the one
 // before it), and the queue of them.
-constexpr uint32_t OFF_WILD = OFF_ORDER + kSorted, OFF_REDO = OFF_WILD + DVB * 4, OFF_QUEUE = OFF_REDO + 32;
+constexpr uint32_t OFF_WILD = OFF_ORDER + kSorted, OFF_REDO = OFF_WILD + DVB * 4, OFF_QUEUE = OFF_REDO + 48;
 constexpr int kQueue = 8;     // no more than the ring's places are unfinished when the item warp looks, and as many when it has
 constexpr uint32_t kSmemBytes = OFF_QUEUE + kQueue * 52 + 1024;  // + alignment of the base
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a block");
@@ -129,7 +129,7 @@ struct Item {
     int third;           // the last chunks, in scan order, whose V' needs its third part
     int rev;
     int careful;         // done again, see above
-    int index;           // among the CTA's items
+    int index;           // among the CTA's items that have chunks
     float l;
 };
 static_assert(sizeof(Item) * kItems <= 512 - 288 && sizeof(Item) <= 52, "the ring's place and the queue's");
@@ -282,11 +282,11 @@ __device__ __forceinline__ void start_y1(uint32_t y1, const int* first, int at) 
         tmem_st8(y1 + d, r);
     }
 }
-// Of 64 columns of the scores, from tile column j0 on, those from n on become zero (rows behind the sequence's end, whatever they
-// hold), and with `careful` those behind the diagonal.
-__device__ __forceinline__ void trim(uint32_t p, int row, int j0, int n, bool careful, bool rev) {
+// And of 64 columns of the scores, from tile column j0 on, those behind the diagonal and those from n on become zero (rows behind
+// the sequence's end: elsewhere the zeros in V's place are enough).
+__device__ __forceinline__ void trim(uint32_t p, int row, int j0, int n, bool rev) {
 #pragma unroll 1
-    for (int j = careful ? 0 : max(0, (n - j0) & ~7); j < 64; j += 8) {
+    for (int j = 0; j < 64; j += 8) {
         float v[8];
         tmem_ld8(p + j, v);
         tmem_wait_ld();
@@ -294,7 +294,7 @@ __device__ __forceinline__ void trim(uint32_t p, int row, int j0, int n, bool ca
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = j0 + j + i;
-            r[i] = c < n && !(careful && (rev ? c < row : c > row)) ? __float_as_uint(v[i]) : 0u;
+            r[i] = c < n && (rev ? c >= row : c <= row) ? __float_as_uint(v[i]) : 0u;
         }
         tmem_st8(p + j, r);
     }
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
     Item* queue = reinterpret_cast<Item*>(sm + OFF_QUEUE);
     volatile int* posted = reinterpret_cast<volatile int*>(sm + OFF_REDO);
-    volatile int *odd = posted + 4, *served = posted + 1;
+    volatile int *odd = posted + 4, *served = posted + 1, *indexed = posted + 8;
     uint64_t* asked = reinterpret_cast<uint64_t*>(sm + OFF_REDO + 8);  // a barrier: the warps of the scores want V
     int* wild = reinterpret_cast<int*>(sm + OFF_WILD);
     constexpr bool kOut = kMode != kStates;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                                   : 1);
             mbar_init(asked, 8);
             *stop = 0;
-            *posted = *served = 0;
+            *posted = *served = *indexed = 0;
             for (int i = 0; i < 4; ++i) odd[i] = 0;
             fence_mbar_init();
         }
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     const int i = put % kItems;
                     if (put >= kItems && !bar_wait(&bars[IEMPTY + i], ((put / kItems) - 1) & 1, stop, kItemWait)) return false;
                     items[i] = it;
-                    items[i].index = put - round;
+                    items[i].index = *indexed;
+                    if (it.nc > 0) *indexed = *indexed + 1;
                     mbar_arrive(&bars[IFULL + i]);
                     ++put;
                     return true;
@@ -472,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 if (!ok) *stop = 1;
                 Item end;
                 end.scan = -1;
+                end.nc = 0;
                 if (!announce(end)) *stop = 1;
             } while (!over());
         } else if (warp == kWarpTma) {
@@ -703,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (!(ok = warp_wait(&bars[GUARD], gc++ & 1, stop))) break;
                         tc_fence_after();
                         start_y1(lane_base + COL_Y1 + j0 / 2, wild + j0 / 2, rev ? C - 1 - row : row);
+                        trim(col, row, j0, n, rev);
                     }
-                    if (careful || n < j0 + 64) trim(col, row, j0, n, careful, rev);
 #pragma unroll
                     for (int b = 0; b < 4; b += 2) {
                         float v[2][16];
@@ -951,21 +953,28 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     finite = finite && (stored <= 0 || zero.x + zero.y == 0.f);
                 }
             }
-            if (kOut && ok) {
-                // Done again by all warps or by none: the final state, which may take the initial one's place, is left until then.
+            if (kOut && ok && it->nc > 0) {
+                // One warp decides for all whether the item is done again.  Where the final state takes the initial one's place they
+                // wait for that, and leave the state until then (in segments, which write none, they wait too: it spills less).  No
+                // warp is here for the next item before all were for this one: its chunks wait for all their copies of S.
+                const bool wait = kMode == kOutputs || prm.scan[it->scan].a.init == prm.scan[it->scan].a.final_state;
                 const int item = it->index;
                 if (!__all_sync(0xffffffffu, finite) && lane == 0) odd[item & 3] = 1;
                 if (warp == kWarpOut && lane == 0) odd[(item + 1) & 3] = 0;
                 warp_arrive(&bars[AGREE], lane);
-                ok = warp_wait(&bars[AGREE], item & 1, stop);
-                if (ok && odd[item & 3] && !it->careful) {
-                    if (warp == kWarpOut && lane == 0) {
-                        queue[*posted % kQueue] = *it;
-                        __threadfence_block();
-                        *posted = *posted + 1;
+                if (wait || warp == kWarpOut) {
+                    ok = warp_wait(&bars[AGREE], item & 1, stop);
+                    if (ok && odd[item & 3] && !it->careful) {
+                        if (warp == kWarpOut && lane == 0) {
+                            queue[*posted % kQueue] = *it;
+                            __threadfence_block();
+                            *posted = *posted + 1;
+                        }
+                        if (wait) {
+                            leave(k);
+                            continue;
+                        }
                     }
-                    leave(k);
-                    continue;
                 }
             }
             if (kMode != kOutputs) {
