@@ -24,8 +24,9 @@
 // Values that are not finite: what the mask multiplies by zero (scores behind the diagonal, and in P V the rows behind an
 // output's own) may be NaN or infinite, and would make outputs NaN that do not depend on it.  A product of such a value with
 // zero is NaN, so no output that is finite is wrong: the warps that write them watch for NaN, and an item that had one is done
-// again carefully.  There the scores behind the diagonal become zero before the mask, one warp takes what is not finite
-// out of V before P V, and Y1 starts as NaN where an output depends on it, else as zero.
+// again carefully.  There the warps of the scores take what is not finite out of V before P V, start Y1 as NaN where an output
+// depends on it, else as zero, and make the scores behind the diagonal zero before the mask (4 x 8192 rows of 64 heads, the
+// second half of them NaN: 974 us, 299 without).
 //
 // 28 warps, one CTA per SM (224 KB of shared memory, 512 TMEM columns):
 //   0-7   P: two warpgroups, 64 columns each: TMEM -> mask -> bf16 back into the same TMEM columns (A operand)
@@ -37,7 +38,7 @@
 //   24    TMA: K, V, Q of a chunk, two or three stages
 //   25    tcgen05.mma
 //   26    the CTA's items
-//   27    V without what is not finite, of the items that are done again
+//   27    tells where V is, for the items that are done again
 // Q, K, V are read once (Q and K once for each 64 value channels, the second time from L2), o written once.  Where heads
 // are many the power limit bounds it: 2 x 8192 rows of 74 heads 128 x 64 take 195 us (4.8 TB/s) at the 1365 MHz that it
 // leaves, and 152 us (6.1 TB/s) on zeros, which draw less, at 1965 MHz; 4 x 8192 rows of 64 heads 354 us.  Where they are
@@ -255,24 +256,31 @@ __device__ __forceinline__ int64_t next_block(const void* answer) {
     return got ? (int64_t)x : -1;
 }
 
-// For items that are done again, by one warp: what is not finite in a V tile becomes zero, and `first` the first row, in scan
-// order, that had such a value in each channel.
-__device__ __forceinline__ void tame(uint8_t* tv, int* first, int lane, bool rev) {
-    first[lane] = first[lane + 32] = C;
-    __syncwarp();
+// For items that are done again, by the eight warps of the scores.  16 rows of a V tile: what is not finite becomes zero, and
+// `first` the first row, in scan order, that had such a value in each channel (C before).
+__device__ __forceinline__ void tame(uint8_t* tv, int* first, int warp, int lane, bool rev) {
+    int a = C, b = C;  // of this lane's two channels
+    const int word = (lane & 3) * 4;
 #pragma unroll 1
-    for (int i = lane; i < C * DVB / 2; i += 32) {  // words of two channels
-        const int row = i / 32, word = i & 31, at = rev ? C - 1 - row : row;
-        uint32_t* p = reinterpret_cast<uint32_t*>(tv + sw128_off(row, word / 4)) + (word & 3);
-        const uint32_t x = *p;
-        const bool lo = (x & 0x7F80u) == 0x7F80u, hi = (x & 0x7F800000u) == 0x7F800000u;
-        if (!lo && !hi) continue;
-        if (lo) atomicMin(first + 2 * word, at);
-        if (hi) atomicMin(first + 2 * word + 1, at);
-        *p = x & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
+    for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 4) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint32_t*>(tv + sw128_off(r0 + i, lane / 4) + word);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = rev ? C - 1 - r0 - i : r0 + i;
+            const bool lo = (x[i] & 0x7F80u) == 0x7F80u, hi = (x[i] & 0x7F800000u) == 0x7F800000u;
+            a = lo ? min(a, at) : a;
+            b = hi ? min(b, at) : b;
+            if (lo || hi)
+                *reinterpret_cast<uint32_t*>(tv + sw128_off(r0 + i, lane / 4) + word) =
+                    x[i] & ((lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u));
+        }
     }
+    if (a < C) atomicMin(first + 2 * lane, a);
+    if (b < C) atomicMin(first + 2 * lane + 1, b);
 }
-// The same, by the warps of the scores: Y1 (32 of its channels) NaN where an output depends on such a value, else zero.
+// Then Y1 (32 of its channels): NaN where an output depends on such a value, else zero.
 __device__ __forceinline__ void start_y1(uint32_t y1, const int* first, int at) {
 #pragma unroll 1
     for (int d = 0; d < 32; d += 8) {
@@ -313,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     Item* queue = reinterpret_cast<Item*>(sm + OFF_QUEUE);
     volatile int* posted = reinterpret_cast<volatile int*>(sm + OFF_REDO);
     volatile int *odd = posted + 4, *served = posted + 1, *indexed = posted + 8;
-    uint64_t* asked = reinterpret_cast<uint64_t*>(sm + OFF_REDO + 8);  // a barrier: the warps of the scores want V
+    // Barriers of the items that are done again: the warps of the scores ask where V is; all of them have done their rows of it.
+    uint64_t *asked = reinterpret_cast<uint64_t*>(sm + OFF_REDO + 8), *tamed = reinterpret_cast<uint64_t*>(sm + OFF_REDO + 40);
+    volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(sm + OFF_REDO + 36);
     int* wild = reinterpret_cast<int*>(sm + OFF_WILD);
     constexpr bool kOut = kMode != kStates;
     constexpr int kMaxParts = kMode == kOutputs ? 2 : 3;  // of V'
@@ -328,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                                     : i >= IEMPTY ? (kOut ? 27 : 26)  // warps that read an item
                                                   : 1);
             mbar_init(asked, 8);
+            mbar_init(tamed, 8);
             *stop = 0;
             *posted = *served = *indexed = 0;
             for (int i = 0; i < 4; ++i) odd[i] = 0;
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             __syncwarp();
             bar_wait(&bars[MMADONE], 0, nullptr, kWait / 20);
         } else if (kOut) {
-            // ---- V of items that are done again, when the warps of the scores ask for it: they follow every chunk, while this one
+            // ---- where V is, of items that are done again, when the warps of the scores ask: they follow every chunk, while this one
             // skips other items' and is ahead of them, so that the parity of another barrier would tell it nothing
             int gc = 0;  // chunks of such items
             Ring ring;
@@ -646,13 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             bool ok = true;
             for (int k = 0; ok && (it = enter(k)) != nullptr; ++k) {
                 ring.cut(prm.scan[it->scan].a.Dk, kOut);
-                const int nc = it->nc, rev = it->rev, careful = it->careful;
+                const int nc = it->nc, careful = it->careful;
                 leave(k);
                 for (int c = 0; ok && c < nc; ++c, ring.step()) {
                     if (!careful) continue;
                     if (!(ok = warp_wait(asked, gc++ & 1, stop))) break;
-                    tame(sm + ring.v(kOut), wild, lane, rev);
-                    fence_async_smem();
+                    wild[lane] = wild[lane + 32] = C;
+                    if (lane == 0) *where = ring.v(kOut);
                     warp_arrive(&bars[GUARD], lane);
                 }
             }
@@ -703,6 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                         if (!ok) break;
                         warp_arrive(asked, lane);
                         if (!(ok = warp_wait(&bars[GUARD], gc++ & 1, stop))) break;
+                        tame(sm + *where, wild, warp, lane, rev);
+                        fence_async_smem();
+                        warp_arrive(tamed, lane);
+                        if (!(ok = warp_wait(tamed, (gc - 1) & 1, stop))) break;
                         tc_fence_after();
                         start_y1(lane_base + COL_Y1 + j0 / 2, wild + j0 / 2, rev ? C - 1 - row : row);
                         trim(col, row, j0, n, rev);
