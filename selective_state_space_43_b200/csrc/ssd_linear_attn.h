@@ -47,9 +47,9 @@ struct ScanArgs {
 //   kOutputs the outputs of each segment from the state in seg_state
 enum Mode { kWhole = 0, kStates = 1, kOutputs = 2 };
 
-// One block's rows: row0 .. row0 + n of sequence `seq`, whose first row is `start`; ok: anything to do.
+// One block's rows: row0 .. row0 + n of sequence `seq`; ok: anything to do.
 struct Segment {
-    int64_t row0, n, start, seq, index;
+    int64_t row0, n, seq;
     bool ok;
 };
 
@@ -80,7 +80,7 @@ __device__ inline int64_t first_slot(const ScanArgs& a, int64_t b, const Span& s
 __device__ inline Segment segment_of(const ScanArgs& a, int64_t slot) {
     if (a.seg_len == 0) {
         const Span s = sequence_span(a, slot);
-        return Segment{s.start, s.len, s.start, slot, 0, true};
+        return Segment{s.start, s.len, slot, true};
     }
     int64_t b;
     if (a.cu) {  // the last sequence whose first slot is not behind this one
@@ -96,8 +96,8 @@ __device__ inline Segment segment_of(const ScanArgs& a, int64_t slot) {
     }
     const Span s = sequence_span(a, b);
     const int64_t i = slot - first_slot(a, b, s), r = i * a.seg_len;
-    if (!s.ok || i < 0 || r >= s.len) return Segment{0, 0, 0, b, i, false};
-    return Segment{s.start + r, s.len - r < a.seg_len ? s.len - r : a.seg_len, s.start, b, i, true};
+    if (!s.ok || i < 0 || r >= s.len) return Segment{0, 0, b, false};
+    return Segment{s.start + r, s.len - r < a.seg_len ? s.len - r : a.seg_len, b, true};
 }
 
 // e^{l n} of a head; -inf (a head that keeps nothing) gives e^{l 0} = 1 like every other decay.
