@@ -253,7 +253,8 @@ cudaError_t launch_scans(const ScanArgs* scans, int count, Mode mode, cudaStream
 // times the mean, each sequence to need `more` segments beside those of its rows.  The constants are fitted to 229 measured
 // cases (B200, every cut of 32 to 8192 rows; sizes drawn at random, packed rows cut at random places): in 224 of
 // them the choice is within 10 % of the fastest, the worst is 22 % off (bf16 backward, 2 sequences of 4932 rows, 8 heads of
-// 64 x 96: 54 us, 44 whole).  Both sides of some, in us as replayed one behind the other, whole against the chosen cut:
+// 64 x 96: 54 us, 44 whole).  Both sides of some, in us, whole against the chosen cut, three replays from an idle GPU (the
+// power cap, which makes the 289 below 333 in a long run, does not bite yet):
 // bf16, 1 x 8191 rows, 16 heads of 128 x 128, 120 against 72 (2048 rows; 90 at 512); 9000 rows in 12, 10 heads of
 // 64 x 64, 37 whole (51 at 512); 4 x 8192 rows, 64 heads of 128 x 64, 289 whole (459 at 2048).  fp32, 1 x 256 rows, 4 heads
 // of 32 x 64, 33 against 17 (32 rows); 4636 rows in 15, 16 heads of 64 x 96, 308 against 253 (128; 321 at 512);

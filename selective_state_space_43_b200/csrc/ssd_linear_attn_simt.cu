@@ -7,7 +7,7 @@
 // in fp32 throughout.  The state lives in registers (Dk/16 x 8 per thread) and is copied to shared memory
 // for the Q S product of the next chunk.  Two groups of warps side by side: scores and outputs, and the state.  Bound by
 // fp32 FMAs, 2 Dk + C per row and value channel and C Dk / 64 for the scores, and the shared-memory reads that feed them:
-// 4 x 1000 rows of 32 heads 128 x 128, 438 us (579 with one group for both).
+// 4 x 1000 rows of 32 heads 128 x 128, 446 us (579 with one group for both).
 #include "ssd_common.cuh"
 #include "ssd_linear_attn.h"
 #include "ssd_internal.h"

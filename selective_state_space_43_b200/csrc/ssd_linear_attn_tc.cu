@@ -40,9 +40,9 @@
 //   26    the CTA's items
 //   27    tells where V is, for the items that are done again
 // Q, K, V are read once (Q and K once for each 64 value channels, the second time from L2), o written once.  Where heads
-// are many the power limit bounds it: 2 x 8192 rows of 74 heads 128 x 64 take 195 us (4.8 TB/s) at the 1365 MHz that it
-// leaves, and 152 us (6.1 TB/s) on zeros, which draw less, at 1965 MHz; 4 x 8192 rows of 64 heads 354 us.  Where they are
-// few, the chain scores - mask - products - outputs of a chunk does: one prompt of 8191 rows, 16 heads 128 x 128, 75 us.
+// are many the power limit bounds it: 2 x 8192 rows of 74 heads 128 x 64 take 182 us (5.1 TB/s) at the 1365 MHz that it
+// leaves, and 151 us (6.2 TB/s) on zeros, which draw less, at 1965 MHz; 4 x 8192 rows of 64 heads 333 us.  Where they are
+// few, the chain scores - mask - products - outputs of a chunk does: one prompt of 8191 rows, 16 heads 128 x 128, 74 us.
 #include "ssd_common.cuh"
 #include "ssd_internal.h"
 #include "ssd_linear_attn.h"
@@ -400,9 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
             const bool sorted = call.cu && call.seg_len == 0 && call.batch <= kSorted && gridDim.x > 148;
             uint8_t* order = sm + OFF_ORDER;
             if (sorted) {
-                // Packed sequences are taken longest first, so that no long one starts when the other SMs run out of work
-                // (24 ragged prompts of 16384 rows in all, 40 heads: 137 -> 122 us); more of them even out by themselves:
-                // sequence i goes to the place that the number of longer ones (and equal ones before it) gives.
+                // Packed sequences are taken longest first, so that no long one starts when the other SMs run out of work (24
+                // ragged prompts of 16384 rows in all, 40 heads: 137 -> 119 us when this was added): sequence i goes to the
+                // place that the number of longer ones (and equal ones before it) gives.  More than kSorted are taken as they
+                // come: of prompts of 200 rows and one of 4000, 16 heads, 64 take 75 us wherever it stands, 65 take 69 us
+                // with it in front and 111 with it at the end.
                 const int n = (int)call.batch;
                 for (int i = lane; i < n; i += 32) {
                     const int len = (int)sequence_span(call, i).len;
