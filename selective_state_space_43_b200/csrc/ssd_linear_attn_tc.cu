@@ -355,19 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
     const int row = (warp & 3) * 32 + lane;  // TMEM lane of a worker thread
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
 
-    // The end of a round, for all warps; true: of the last.  The second round is for the items that are to be done again and were
+    // The end of a lap, for all warps; true: of the last.  The second lap is for the items that are to be done again and were
     // not yet when the first ended.
-    int round = 0;
+    int lap = 0;
     auto over = [&] {
         __syncwarp();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        return !kOut || round++ == 1 || *posted == *served || *stop;
+        return !kOut || lap++ == 1 || *posted == *served || *stop;
     };
     // Gives back a place of the ring, after the role has copied what it needs.
     auto leave = [&](int number) { warp_arrive(&bars[IEMPTY + number % kItems], lane); };
-    // A place of the ring, or nullptr: no more, and the last round is over.
+    // A place of the ring, or nullptr: no more, and the last lap is over.
     auto enter = [&](int& number) -> const Item* {
         for (;; ++number) {
             const int i = number % kItems;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            int put = 0, taken = 0;  // announced (the first round's end too), and of the queue of items to be done again
+            int put = 0, taken = 0;  // announced (the first lap's end too), and of the queue of items to be done again
             do {
                 if (lane != 0) continue;
                 int64_t block = blockIdx.x;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     return true;
                 };
                 // the loads of the item announced last are due to end
-                auto loaded = [&] { return bar_wait(&bars[LASTLOAD], (put - round - 1) & 1, stop, kItemWait); };
+                auto loaded = [&] { return bar_wait(&bars[LASTLOAD], (put - lap - 1) & 1, stop, kItemWait); };
                 auto again = [&] {
                     while (kOut && taken != *posted) {
                         __threadfence_block();
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1) scan_tc_kernel(const __grid_const
                     return true;
                 };
                 bool ok = true;
-                if (round == 1) ok = again();
-                for (int asks = 0; round == 0; ++asks) {
+                if (lap == 1) ok = again();
+                for (int asks = 0; lap == 0; ++asks) {
                     Item it;
                     it.scan = 0;
                     unsigned b = (unsigned)block;
